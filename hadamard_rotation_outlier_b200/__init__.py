@@ -25,6 +25,11 @@ from .binding import (  # noqa: F401
     hadq_last_error,
     hadq_launch_count,
     hadq_kron_plan,
+    hadq_paged_append,
+    hadq_paged_attention,
+    hadq_paged_gather,
+    hadq_paged_slots,
+    hadq_paged_workspace_size,
     hadq_plan,
     hadq_rotate_quantize,
     hadq_rotate_quantize_asym,

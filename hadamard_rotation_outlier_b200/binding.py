@@ -27,7 +27,8 @@ EXPORTED = ("hadq_rotate_quantize", "hadq_dequant_rotate_inv", "hadq_rotate_quan
             "hadq_dequant_rotate_inv_kron", "hadq_rotate_quantize_kron_pm1", "hadq_dequant_rotate_inv_kron_pm1", "hadq_rotate_quantize_asym",
             "hadq_dequant_rotate_inv_asym", "hadq_rotate_quantize_keep",
             "hadq_dequant_rotate_inv_keep", "hadq_kv_decode_attention",
-            "hadq_kv_decode_workspace_size", "hadq_kv_decode_attention_noalloc", "hadq_plan", "hadq_kron_plan", "hadq_device_status", "hadq_selftest_bounded_wait", "hadq_status_str", "hadq_last_error",
+            "hadq_kv_decode_workspace_size", "hadq_kv_decode_attention_noalloc",
+            "hadq_paged_slots", "hadq_paged_append", "hadq_paged_gather", "hadq_paged_attention", "hadq_paged_workspace_size", "hadq_plan", "hadq_kron_plan", "hadq_device_status", "hadq_selftest_bounded_wait", "hadq_status_str", "hadq_last_error",
             "hadq_launch_count", "hadq_version")
 
 
@@ -88,6 +89,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.hadq_kv_decode_workspace_size.argtypes = [c_i32, c_i32, c_i32, c_i64,
                                                   ctypes.POINTER(ctypes.c_size_t)]
     lib.hadq_kv_decode_workspace_size.restype = ctypes.c_int
+    lib.hadq_paged_slots.argtypes = [vp, vp, c_i32, vp, c_i32, c_i32, vp, c_i32, vp, vp, vp, c_i64, vp, vp]
+    lib.hadq_paged_slots.restype = ctypes.c_int
+    lib.hadq_paged_append.argtypes = [vp, vp, c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, vp, c_i32, c_i32, vp,
+                                      vp, vp, vp, vp, c_i64, c_i32, vp]
+    lib.hadq_paged_append.restype = ctypes.c_int
+    lib.hadq_paged_gather.argtypes = [vp, vp, c_i64, c_i32, c_i32, c_i32, c_i32, vp, c_i32, c_i32, vp, c_i64, vp,
+                                      ctypes.c_int, vp]
+    lib.hadq_paged_gather.restype = ctypes.c_int
+    lib.hadq_paged_attention.argtypes = [vp, c_i64, c_i64, vp, vp, c_i32, c_i32, vp, vp, vp, vp, c_i64, c_i32, vp,
+                                         c_i32, c_i32, c_i32, c_i32, c_i32, vp, c_i32, c_i32, c_i32, c_i32, c_i32,
+                                         ctypes.c_float, vp, vp, ctypes.c_size_t, vp]
+    lib.hadq_paged_attention.restype = ctypes.c_int
+    lib.hadq_paged_workspace_size.argtypes = [c_i32, c_i32, c_i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.hadq_paged_workspace_size.restype = ctypes.c_int
     lib.hadq_plan.argtypes = [c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32,
                               ctypes.POINTER(ctypes.c_int)]
     lib.hadq_plan.restype = ctypes.c_int
@@ -377,6 +392,225 @@ def hadq_kv_decode_attention_noalloc(q: torch.Tensor, k_codes: torch.Tensor, k_s
         _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), batch, nqh, nkv,
         stride if tokens is None else tokens, stride, dim, block, _ptr(signs), bits, group,
         float(softmax_scale), _ptr(out), code, _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------- paged KV cache
+
+def _on_device(t, name, dtype, device, shape=None):
+    """A contiguous tensor of this type on this device (and of this shape)."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, name, dtype, device)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _call(fn, device, stream, *args):
+    """Call a C entry point on the tensors' device: ``args`` and the stream
+    (its current stream when none is given)."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_view(t, name, device, heads):
+    """Row stride of a bf16 [tokens, heads, dim] tensor whose tokens are
+    contiguous rows at any stride (a slice of a wider projection)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, dim], got {list(t.shape)}")
+    n, h, d = t.shape
+    if t.stride(2) != 1 and d > 1 or t.stride(1) != d and h > 1:
+        raise ValueError(f"{name} must hold each token's [heads, dim] contiguously")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _pool(codes, scales, name, device, bits, group, shape=None):
+    """Check one tensor of the pool; its [n_pages, n_kv_heads, page_size, bytes]."""
+    if codes.dim() != 4:
+        raise ValueError(f"{name}_codes must be [n_pages, n_kv_heads, page_size, dim*bits/8], got {list(codes.shape)}")
+    if codes.dtype is torch.int8:  # INT8 caches may come as int8
+        codes = codes.view(torch.uint8)
+    _on_device(codes, f"{name}_codes", torch.uint8, device, shape)
+    if codes.shape[3] != 16 * bits:
+        raise ValueError(f"{name}_codes rows hold {codes.shape[3]} bytes, expected 128*bits/8 = {16 * bits}")
+    _on_device(scales, f"{name}_scales", torch.float32, device)
+    per = 128 // group if group > 0 and 128 % group == 0 else 1
+    if scales.numel() != codes.shape[0] * codes.shape[1] * codes.shape[2] * per or scales.shape[:3] != codes.shape[:3]:
+        raise ValueError(f"{name}_scales must be [n_pages, n_kv_heads, page_size, dim/group], got {list(scales.shape)}")
+    return codes.shape
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def hadq_paged_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                     block_table: torch.Tensor, page_size: int, capacity: int | None = None,
+                     slots: torch.Tensor | None = None, total_lens: torch.Tensor | None = None,
+                     cu_new: torch.Tensor | None = None, counts: torch.Tensor | None = None, stream=None):
+    """Block tables and slots of the tokens that join a paged cache.
+
+    ``cached_lens``/``new_lens``: int32 ``[batch]``; ``free_pages``: int32
+    ``[n_free]``; ``block_table``: int32 ``[batch, max_pages]``, whose entries
+    for the new pages are written.  ``capacity`` rows of ``slots`` are filled
+    (pass either; -1 behind the last new token).  Returns ``(slots,
+    total_lens, cu_new, counts)`` with ``counts = [pages taken, requests
+    refused]``; a refused request has total length 0 and slots -1.
+    """
+    lib = load_library()
+    dev = _cuda(cached_lens, "cached_lens")
+    batch = cached_lens.numel()
+    _on_device(cached_lens, "cached_lens", torch.int32, dev, (batch,))
+    _on_device(new_lens, "new_lens", torch.int32, dev, (batch,))
+    _on_device(free_pages, "free_pages", torch.int32, dev, (free_pages.numel(),))
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, max_pages], got {list(block_table.shape)}")
+    _on_device(block_table, "block_table", torch.int32, dev)
+    if slots is None:
+        if capacity is None:
+            raise ValueError("pass capacity (the rows of slots to fill) or slots")
+        slots = torch.empty(capacity, dtype=torch.int32, device=dev)
+    else:
+        _on_device(slots, "slots", torch.int32, dev, (slots.numel() if capacity is None else capacity,))
+    outs = []
+    for name, t, n in (("total_lens", total_lens, batch), ("cu_new", cu_new, batch + 1), ("counts", counts, 2)):
+        if t is None:
+            t = torch.empty(n, dtype=torch.int32, device=dev)
+        else:
+            _on_device(t, name, torch.int32, dev, (n,))
+        outs.append(t)
+    total_lens, cu_new, counts = outs
+    _call(lib.hadq_paged_slots, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(), batch, free_pages.data_ptr(),
+          free_pages.numel(), page_size, block_table.data_ptr(), block_table.shape[1], total_lens.data_ptr(),
+          cu_new.data_ptr(), slots.data_ptr(), slots.numel(), counts.data_ptr())
+    return slots, total_lens, cu_new, counts
+
+
+def hadq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
+                      k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor, block: int = -1,
+                      signs: torch.Tensor | None = None, bits: int = 4, group: int = -1, stream=None) -> None:
+    """Rotate and quantise the K and V rows of new tokens into their slots.
+
+    ``k``/``v``: bf16 ``[tokens, n_kv_heads, 128]``, each token's row
+    contiguous (slices of a wider projection are fine).  ``slots``: int32
+    ``[tokens]``; tokens whose slot is outside the pool are skipped.  The pool:
+    codes uint8 (or int8) ``[n_pages, n_kv_heads, page_size, 128*bits/8]``,
+    scales float32 ``[n_pages, n_kv_heads, page_size, 128/group]`` (the
+    trailing 1 may be dropped).
+    """
+    lib = load_library()
+    dev = _cuda(k, "k")
+    dim = k.shape[-1] if k.dim() else 0
+    G = _resolve(dim, block, group)
+    shape = _pool(k_codes, k_scales, "k", dev, bits, G)
+    _pool(v_codes, v_scales, "v", dev, bits, G, tuple(shape))
+    ks, vs = _rows_view(k, "k", dev, shape[1]), _rows_view(v, "v", dev, shape[1])
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    _on_device(slots, "slots", torch.int32, dev, (k.shape[0],))
+    if signs is not None:
+        _on_device(signs, "signs", torch.int8, dev, (dim,))
+    _call(lib.hadq_paged_append, dev, stream, k.data_ptr(), v.data_ptr(), k.shape[0], ks, vs, shape[1], dim, block, _at(signs),
+          bits, group, slots.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+          shape[0], shape[2])
+
+
+def hadq_paged_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, block: int = -1,
+                      signs: torch.Tensor | None = None, bits: int = 4, group: int = -1,
+                      out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                      stream=None) -> torch.Tensor:
+    """Read rows of a paged cache back: dequantise and undo the rotation.
+
+    Returns ``[tokens, n_kv_heads, 128]`` bf16 or fp32.  Rows whose slot is
+    outside the pool are left as they were (of a new ``out``: undefined).
+    """
+    lib = load_library()
+    dev = _cuda(codes, "codes")
+    shape = _pool(codes, scales, "pool", dev, bits, _resolve(128, block, group))
+    _on_device(slots, "slots", torch.int32, dev, (slots.numel(),))
+    if signs is not None:
+        _on_device(signs, "signs", torch.int8, dev, (128,))
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bfloat16 or float32")
+    want = (slots.numel(), shape[1], 128)
+    if out is None:
+        out = torch.empty(want, dtype=out_dtype, device=dev)
+    else:
+        _on_device(out, "out", out_dtype, dev, want)
+    _call(lib.hadq_paged_gather, dev, stream, codes.data_ptr(), scales.data_ptr(), shape[0], shape[2], shape[1], 128, block,
+          _at(signs), bits, group, slots.data_ptr(), slots.numel(), out.data_ptr(),
+          HADQ_OUT_F32 if out_dtype == torch.float32 else HADQ_OUT_BF16)
+    return out
+
+
+def hadq_paged_workspace_size(max_new: int, n_q_heads: int, n_kv_heads: int) -> int:
+    """Host-only: workspace bytes :func:`hadq_paged_attention` needs (any GPU, batch and lengths)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().hadq_paged_workspace_size(max_new, n_q_heads, n_kv_heads, ctypes.byref(n)))
+    return int(n.value)
+
+
+def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                         v_scales: torch.Tensor, block_table: torch.Tensor, total_lens: torch.Tensor,
+                         cu_new: torch.Tensor, max_new: int, block: int = -1, signs: torch.Tensor | None = None,
+                         bits: int = 4, group: int = -1, causal: bool = True, window: int = 0, sinks: int = 0,
+                         softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each request's new tokens over its pages.
+
+    ``q``: bf16 ``[rows, n_q_heads, 128]``, each row contiguous; request b's
+    queries are rows ``cu_new[b]`` to ``cu_new[b + 1]``, at most ``max_new`` of
+    them.  The pool as for :func:`hadq_paged_append`; ``block_table`` int32
+    ``[batch, max_pages]``, ``total_lens`` int32 ``[batch]``, ``cu_new`` int32
+    ``[batch + 1]``.  Causal queries are the last of their request's cached
+    tokens; ``window`` and ``sinks`` limit what they see to the last
+    ``window`` and the first ``sinks`` keys.  ``workspace``: a zero-filled
+    uint8 tensor of at least :func:`hadq_paged_workspace_size` bytes, reused
+    across calls (one is allocated when omitted).  Returns bf16 ``[rows,
+    n_q_heads, 128]``; rows behind the last request are left as they were.
+    """
+    lib = load_library()
+    dev = _cuda(q, "q")
+    stride = _rows_view(q, "q", dev, None)
+    rows, nqh, dim = q.shape
+    shape = _pool(k_codes, k_scales, "k", dev, bits, _resolve(128, block, group))
+    _pool(v_codes, v_scales, "v", dev, bits, _resolve(128, block, group), tuple(shape))
+    batch = total_lens.numel()
+    _on_device(total_lens, "total_lens", torch.int32, dev, (batch,))
+    _on_device(cu_new, "cu_new", torch.int32, dev, (batch + 1,))
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, max_pages], got {list(block_table.shape)}")
+    _on_device(block_table, "block_table", torch.int32, dev)
+    if signs is not None:
+        _on_device(signs, "signs", torch.int8, dev, (dim,))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / float(dim) ** 0.5
+    if out is None:
+        out = torch.empty((rows, nqh, dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _on_device(out, "out", torch.bfloat16, dev, (rows, nqh, dim))
+    if workspace is None:
+        workspace = torch.zeros(hadq_paged_workspace_size(max_new, nqh, shape[1]), dtype=torch.uint8, device=dev)
+    else:
+        _on_device(workspace, "workspace", torch.uint8, dev)
+    _call(lib.hadq_paged_attention, dev, stream, q.data_ptr(), rows, stride, cu_new.data_ptr(), total_lens.data_ptr(), batch,
+          max_new, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), shape[0], shape[2],
+          block_table.data_ptr(), block_table.shape[1], nqh, shape[1], dim, block, _at(signs), bits, group, int(causal),
+          window, sinks, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 

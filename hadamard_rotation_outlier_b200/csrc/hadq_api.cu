@@ -26,6 +26,8 @@
 #include "hadq_h4096.cuh"
 #include "hadq_h4096_tc.cuh"
 #include "hadq_kron.cuh"
+#include "hadq_paged.cuh"
+#include "hadq_paged_attn.cuh"
 #include "hadq_kernels.h"
 
 namespace {
@@ -1196,6 +1198,288 @@ hadq_status hadq_dequant_rotate_inv_kron_pm1(const void* codes, const float* sca
                                              int32_t group, void* out, hadq_out_dtype out_dtype,
                                              hadq_stream_t stream) {
   return kron_inverse(true, codes, scales, rows, a, nullptr, sa, b, signs, bits, group, out, out_dtype, stream);
+}
+
+// ------------------------------------------------------ paged KV cache
+
+struct PagedShape {
+  int ng, page_log2;
+  uint32_t nslots;  // n_pages * page_size
+};
+
+static hadq_status paged_check(int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t dim, int32_t block,
+                               int32_t bits, int32_t group, PagedShape* p) {
+  Shape s;
+  const hadq_status st = check_sizes(0, dim, block, bits, group, &s);
+  if (st != HADQ_OK) return st;
+  if (n_kv_heads < 1) return fail(HADQ_ERR_INVALID_ARG, "n_kv_heads must be >= 1 (got %d)", n_kv_heads);
+  if (n_pages < 0) return fail(HADQ_ERR_INVALID_ARG, "n_pages must be >= 0 (got %lld)", (long long)n_pages);
+  if (!is_pow2(page_size) || page_size < 16 || page_size > 1024)
+    return fail(HADQ_ERR_INVALID_ARG, "page_size must be a power of two in [16, 1024] (got %d)", page_size);
+  if (dim != hadq::kPagedDim || s.B != hadq::kPagedDim || (s.G != 128 && s.G != 64 && s.G != 32))
+    return fail(HADQ_ERR_UNSUPPORTED, "the paged cache supports dim 128, block 128, group 128, 64 or 32 (got %d, %d, %d)",
+                dim, s.B, s.G);
+  if (n_pages > 0x7fffffff / page_size)
+    return fail(HADQ_ERR_UNSUPPORTED, "n_pages * page_size must be below 2^31 (got %lld * %d)", (long long)n_pages,
+                page_size);
+  p->ng = hadq::kPagedDim / s.G;
+  p->page_log2 = ilog2(page_size);
+  p->nslots = uint32_t(n_pages * page_size);
+  return HADQ_OK;
+}
+
+static hadq_status launch_paged(const void* fn, int64_t grid, int threads, void* args, size_t smem, const char* what,
+                                hadq_stream_t stream) {
+  void* argv[] = {args};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned(grid)), dim3(unsigned(threads)), argv, smem,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return fail(HADQ_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+  }
+  return after_launch(what);
+}
+
+// Grid of a grid-stride kernel over `tiles` warps' worth of work: one wave.
+static int64_t paged_wave(int64_t tiles, int warps, int resident) {
+  const int64_t need = (tiles + warps - 1) / warps, wave = int64_t(resident) * sm_count();
+  return need < wave ? need : wave;
+}
+
+hadq_status hadq_paged_slots(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                             const int32_t* free_pages, int32_t n_free, int32_t page_size, int32_t* block_table,
+                             int32_t max_pages, int32_t* total_lens, int32_t* cu_new, int32_t* slots,
+                             int64_t capacity, int32_t* counts, hadq_stream_t stream) {
+  if (batch < 0) return fail(HADQ_ERR_INVALID_ARG, "batch must be >= 0 (got %d)", batch);
+  if (n_free < 0 || max_pages < 0 || capacity < 0)
+    return fail(HADQ_ERR_INVALID_ARG, "n_free, max_pages and capacity must be >= 0 (got %d, %d, %lld)", n_free,
+                max_pages, (long long)capacity);
+  if (!is_pow2(page_size) || page_size < 16 || page_size > 1024)
+    return fail(HADQ_ERR_INVALID_ARG, "page_size must be a power of two in [16, 1024] (got %d)", page_size);
+  if (batch > hadq::kSlotsMaxBatch)
+    return fail(HADQ_ERR_UNSUPPORTED, "batch must be at most %d (got %d)", hadq::kSlotsMaxBatch, batch);
+  if (capacity > 0x7fffffff) return fail(HADQ_ERR_UNSUPPORTED, "capacity must be below 2^31");
+  if (!cu_new || !counts || (batch && (!cached_lens || !new_lens || !total_lens)) || (batch && max_pages && !block_table) ||
+      (n_free && !free_pages) || (capacity && !slots))
+    return fail(HADQ_ERR_INVALID_ARG, "the length, table, free-list and output arrays must not be NULL");
+  for (const void* p : {(const void*)cached_lens, (const void*)new_lens, (const void*)free_pages,
+                        (const void*)block_table, (const void*)total_lens, (const void*)cu_new, (const void*)slots,
+                        (const void*)counts})
+    if (!aligned(p, 4)) return fail(HADQ_ERR_MISALIGNED, "every array must be 4-byte aligned");
+  if (batch && (total_lens == cached_lens || total_lens == new_lens))
+    return fail(HADQ_ERR_INVALID_ARG, "total_lens must not be one of the input arrays");
+  hadq::SlotsArgs a{};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.free_pages = free_pages;
+  a.table = block_table;
+  a.total = total_lens;
+  a.cu = cu_new;
+  a.slots = slots;
+  a.counts = counts;
+  a.capacity = capacity;
+  a.batch = batch;
+  a.n_free = n_free;
+  a.max_pages = max_pages;
+  a.page_log2 = ilog2(page_size);
+  const void* fn = hadq::paged_slots_kernel_ptr();
+  const size_t smem = 2 * (size_t(batch) + 1) * sizeof(uint32_t);
+  int res = 1;
+  const hadq_status st = prepare(fn, hadq::kSlotsThreads, smem, "paged slots kernel", &res);
+  if (st != HADQ_OK) return st;
+  int64_t grid = paged_wave(capacity > batch ? capacity : batch, hadq::kSlotsThreads, 1);
+  if (grid < 1) grid = 1;
+  return launch_paged(fn, grid, hadq::kSlotsThreads, &a, smem, "paged slots kernel", stream);
+}
+
+hadq_status hadq_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                              int32_t n_kv_heads, int32_t dim, int32_t block, const int8_t* signs, int32_t bits,
+                              int32_t group, const int32_t* slots, void* k_codes, float* k_scales, void* v_codes,
+                              float* v_scales, int64_t n_pages, int32_t page_size, hadq_stream_t stream) {
+  PagedShape p;
+  const hadq_status st = paged_check(n_pages, page_size, n_kv_heads, dim, block, bits, group, &p);
+  if (st != HADQ_OK) return st;
+  if (tokens < 0) return fail(HADQ_ERR_INVALID_ARG, "tokens must be >= 0 (got %lld)", (long long)tokens);
+  const int64_t width = int64_t(n_kv_heads) * dim;
+  if (k_stride < width || v_stride < width)
+    return fail(HADQ_ERR_INVALID_ARG, "k_stride and v_stride must be at least n_kv_heads * dim = %lld (got %lld, %lld)",
+                (long long)width, (long long)k_stride, (long long)v_stride);
+  if (tokens == 0 || n_pages == 0) return HADQ_OK;
+  if (!k || !v || !slots || !k_codes || !v_codes || !k_scales || !v_scales)
+    return fail(HADQ_ERR_INVALID_ARG, "k, v, slots, codes and scales must not be NULL");
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8)
+    return fail(HADQ_ERR_MISALIGNED, "k and v rows must be 16-byte aligned (strides multiples of 8)");
+  if (!aligned(k_codes, 16) || !aligned(v_codes, 16))
+    return fail(HADQ_ERR_MISALIGNED, "k_codes and v_codes must be 16-byte aligned");
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(slots, 4))
+    return fail(HADQ_ERR_MISALIGNED, "scales and slots must be 4-byte aligned");
+  hadq::AppendArgs a{};
+  a.x[0] = static_cast<const uint16_t*>(k);
+  a.x[1] = static_cast<const uint16_t*>(v);
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.codes[0] = static_cast<uint8_t*>(k_codes);
+  a.codes[1] = static_cast<uint8_t*>(v_codes);
+  a.scales[0] = k_scales;
+  a.scales[1] = v_scales;
+  a.slots = slots;
+  a.signs = signs;
+  a.rows = tokens * n_kv_heads;
+  a.nslots = p.nslots;
+  a.heads = n_kv_heads;
+  a.page_log2 = p.page_log2;
+  a.scale_mul = (float)(1.0 / (std::sqrt(double(dim)) * (bits == 8 ? 127.0 : 7.0)));
+  const void* fn = hadq::paged_append_kernel_ptr(bits, p.ng, signs != nullptr);
+  int res = 1;
+  const hadq_status pst = prepare(fn, hadq::kAppendThreads, 0, "paged append kernel", &res);
+  if (pst != HADQ_OK) return pst;
+  const int64_t grid = paged_wave(2 * ((a.rows + 15) / 16), hadq::kAppendThreads / 32, res);
+  return launch_paged(fn, grid, hadq::kAppendThreads, &a, 0, "paged append kernel", stream);
+}
+
+hadq_status hadq_paged_gather(const void* codes, const float* scales, int64_t n_pages, int32_t page_size,
+                              int32_t n_kv_heads, int32_t dim, int32_t block, const int8_t* signs, int32_t bits,
+                              int32_t group, const int32_t* slots, int64_t tokens, void* out,
+                              hadq_out_dtype out_dtype, hadq_stream_t stream) {
+  PagedShape p;
+  const hadq_status st = paged_check(n_pages, page_size, n_kv_heads, dim, block, bits, group, &p);
+  if (st != HADQ_OK) return st;
+  if (tokens < 0) return fail(HADQ_ERR_INVALID_ARG, "tokens must be >= 0 (got %lld)", (long long)tokens);
+  if (out_dtype != HADQ_OUT_BF16 && out_dtype != HADQ_OUT_F32)
+    return fail(HADQ_ERR_INVALID_ARG, "out_dtype must be HADQ_OUT_BF16 or HADQ_OUT_F32");
+  if (tokens == 0 || n_pages == 0) return HADQ_OK;
+  if (!codes || !scales || !slots || !out)
+    return fail(HADQ_ERR_INVALID_ARG, "codes, scales, slots and out must not be NULL");
+  if (!aligned(codes, 16) || !aligned(out, 16)) return fail(HADQ_ERR_MISALIGNED, "codes and out must be 16-byte aligned");
+  if (!aligned(scales, 4) || !aligned(slots, 4))
+    return fail(HADQ_ERR_MISALIGNED, "scales and slots must be 4-byte aligned");
+  hadq::GatherArgs a{};
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.scales = scales;
+  a.slots = slots;
+  a.signs = signs;
+  a.out = out;
+  a.rows = tokens * n_kv_heads;
+  a.nslots = p.nslots;
+  a.heads = n_kv_heads;
+  a.page_log2 = p.page_log2;
+  const void* fn = hadq::paged_gather_kernel_ptr(bits, p.ng, out_dtype == HADQ_OUT_F32);
+  int res = 1;
+  const hadq_status pst = prepare(fn, hadq::kGatherThreads, 0, "paged gather kernel", &res);
+  if (pst != HADQ_OK) return pst;
+  const int64_t grid = paged_wave((a.rows + 15) / 16, hadq::kGatherThreads / 32, res);
+  return launch_paged(fn, grid, hadq::kGatherThreads, &a, 0, "paged gather kernel", stream);
+}
+
+// Workspace: arrival counters, then (m, l) and O of two partial units per CTA.
+constexpr int kPagedMaxCtas = 640;
+constexpr size_t kPagedCounterBytes = 8192;
+static size_t paged_part_bytes(int64_t ctas, int rows) { return size_t(ctas) * 2 * rows * (hadq::kPagedDim + 2) * sizeof(float); }
+
+static hadq_status paged_heads_check(int32_t max_new, int32_t nqh, int32_t nkv) {
+  if (max_new < 0) return fail(HADQ_ERR_INVALID_ARG, "max_new must be >= 0 (got %d)", max_new);
+  if (nqh < 1 || nkv < 1)
+    return fail(HADQ_ERR_INVALID_ARG, "n_q_heads and n_kv_heads must be >= 1 (got %d, %d)", nqh, nkv);
+  if (nqh % nkv) return fail(HADQ_ERR_INVALID_ARG, "n_q_heads %d is not a multiple of n_kv_heads %d", nqh, nkv);
+  return HADQ_OK;
+}
+
+hadq_status hadq_paged_workspace_size(int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads, size_t* bytes) {
+  const hadq_status st = paged_heads_check(max_new, n_q_heads, n_kv_heads);
+  if (st != HADQ_OK) return st;
+  if (!bytes) return fail(HADQ_ERR_INVALID_ARG, "bytes must not be NULL");
+  const int64_t rows = int64_t(max_new) * (n_q_heads / n_kv_heads);
+  *bytes = kPagedCounterBytes + paged_part_bytes(kPagedMaxCtas, rows <= 8 ? 8 : 16);
+  return HADQ_OK;
+}
+
+hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride, const int32_t* cu_new,
+                                 const int32_t* total_lens, int32_t batch, int32_t max_new, const void* k_codes,
+                                 const float* k_scales, const void* v_codes, const float* v_scales, int64_t n_pages,
+                                 int32_t page_size, const int32_t* block_table, int32_t max_pages, int32_t n_q_heads,
+                                 int32_t n_kv_heads, int32_t dim, int32_t block, const int8_t* signs, int32_t bits,
+                                 int32_t group, int32_t causal, int32_t window, int32_t sinks, float softmax_scale,
+                                 void* out, void* workspace, size_t workspace_bytes, hadq_stream_t stream) {
+  PagedShape p;
+  hadq_status st = paged_check(n_pages, page_size, n_kv_heads, dim, block, bits, group, &p);
+  if (st != HADQ_OK) return st;
+  st = paged_heads_check(max_new, n_q_heads, n_kv_heads);
+  if (st != HADQ_OK) return st;
+  if (batch < 0 || q_rows < 0 || max_pages < 0)
+    return fail(HADQ_ERR_INVALID_ARG, "batch, q_rows and max_pages must be >= 0 (got %d, %lld, %d)", batch,
+                (long long)q_rows, max_pages);
+  if (q_stride < int64_t(n_q_heads) * dim)
+    return fail(HADQ_ERR_INVALID_ARG, "q_stride must be at least n_q_heads * dim = %lld (got %lld)",
+                (long long)n_q_heads * dim, (long long)q_stride);
+  if (window < 0 || sinks < 0)
+    return fail(HADQ_ERR_INVALID_ARG, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
+  if (!causal && window) return fail(HADQ_ERR_INVALID_ARG, "a window needs causal attention");
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return fail(HADQ_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
+  if (q_rows * n_q_heads > 0x7fffffff)
+    return fail(HADQ_ERR_UNSUPPORTED, "q_rows * n_q_heads must be below 2^31 (got %lld * %d)", (long long)q_rows, n_q_heads);
+  if (max_pages > (1 << 30) / page_size)
+    return fail(HADQ_ERR_UNSUPPORTED, "max_pages * page_size must be at most 2^30 (got %d * %d)", max_pages, page_size);
+  if (batch == 0 || q_rows == 0 || max_new == 0) return HADQ_OK;
+  if (!q || !cu_new || !total_lens || !out || !workspace || (max_pages && !block_table) ||
+      (n_pages && (!k_codes || !k_scales || !v_codes || !v_scales)))
+    return fail(HADQ_ERR_INVALID_ARG, "q, lengths, cache, table, out and workspace must not be NULL");
+  if (!aligned(q, 16) || q_stride % 8) return fail(HADQ_ERR_MISALIGNED, "q rows must be 16-byte aligned (q_stride a multiple of 8)");
+  if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scales, 16) || !aligned(v_scales, 16))
+    return fail(HADQ_ERR_MISALIGNED, "codes and scales must be 16-byte aligned");
+  if (!aligned(cu_new, 4) || !aligned(total_lens, 4) || !aligned(block_table, 4))
+    return fail(HADQ_ERR_MISALIGNED, "cu_new, total_lens and block_table must be 4-byte aligned");
+  if (!aligned(out, 16)) return fail(HADQ_ERR_MISALIGNED, "out must be 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(HADQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  size_t need = 0;
+  hadq_paged_workspace_size(max_new, n_q_heads, n_kv_heads, &need);
+  if (workspace_bytes < need)
+    return fail(HADQ_ERR_INVALID_ARG, "workspace of %zu bytes is below the %zu bytes needed", workspace_bytes, need);
+
+  hadq::PagedAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.q_rows = q_rows;
+  a.signs = signs;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.table = block_table;
+  a.lens = total_lens;
+  a.cu = cu_new;
+  a.out = static_cast<uint16_t*>(out);
+  a.batch = batch;
+  a.nqh = n_q_heads;
+  a.nkv = n_kv_heads;
+  a.g = n_q_heads / n_kv_heads;
+  a.page_log2 = p.page_log2;
+  a.max_pages = max_pages;
+  a.n_pages = int(n_pages);
+  a.causal = causal != 0;
+  a.window = window;
+  a.sinks = sinks;
+  a.qmul = (float)(double(softmax_scale) * 1.4426950408889634 / std::sqrt(double(dim)));
+  a.inv_sqrt_dim = (float)(1.0 / std::sqrt(double(dim)));
+  a.counters = static_cast<unsigned*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes);
+
+  const int64_t rows = int64_t(max_new) * a.g;
+  const int rg = rows <= 8 ? 1 : 2;
+  size_t smem = 0;
+  const void* fn = hadq::paged_decode_kernel_ptr(rg, p.ng, bits, &smem);
+  int res = 1;
+  st = prepare(fn, hadq::kPdThreads, smem, "paged attention kernel (few rows)", &res);
+  if (st != HADQ_OK) return st;
+  int64_t grid = int64_t(res) * sm_count();
+  if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+  a.row_lo = 0;
+  a.row_hi = 0x7fffffff;
+  a.min_tiles = 1;
+  a.part_o = part;
+  a.part_ml = part + grid * 2 * 8 * rg * hadq::kPagedDim;
+  return launch_paged(fn, grid, hadq::kPdThreads, &a, smem, "paged attention kernel (few rows)", stream);
 }
 
 const char* hadq_status_str(hadq_status st) {

@@ -71,4 +71,12 @@ size_t kv_decode_attn_smem(int ng, int bits);
 // of kAttnStaticScratchBytes, or NULL if the runtime cannot resolve it.
 void* attn_static_scratch();
 
+// The paged KV cache (head dim 128; ng as above).
+const void* paged_slots_kernel_ptr();
+const void* paged_append_kernel_ptr(int bits, int ng, bool signs);
+const void* paged_gather_kernel_ptr(int bits, int ng, bool f32);
+// Attention over it for units of 8 * rg query rows (rg = 1, 2); writes the
+// dynamic shared memory it needs to *smem.
+const void* paged_decode_kernel_ptr(int rg, int ng, int bits, size_t* smem);
+
 }  // namespace hadq

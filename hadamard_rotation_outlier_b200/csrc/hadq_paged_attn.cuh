@@ -1,0 +1,753 @@
+// Attention of new tokens over the paged, rotated, quantised KV cache: what
+// both kernels share (arguments, requests, the cut of the work), and the
+// kernel for requests with few query rows.
+//
+//   q_rot = (q * s) H,  score = scale * q_rot . (kcode * kscale)  (= scale * q . k),
+//   p = softmax over the visible keys,  out = ((sum p vcode vscale) H) * s.
+//
+// Query token i of a request with `len` cached tokens (its n new ones among
+// them) sits at position len - n + i and sees the keys at positions up to its
+// own (causal), of these only the first `sinks` and the last `window` when a
+// window is set; without causal it sees all `len` keys.
+//
+// A request's query rows against one KV head are its tokens times the g query
+// heads that share the head (row = token * g + head).  A unit is a group of
+// such rows; all units' key tiles, in the order (request, KV head, row group),
+// form one line that is cut into equal pieces, one per CTA.  So the load is
+// even whatever the lengths, a long request is split over many CTAs and a
+// short one is not, and at most the first and the last unit of a CTA are
+// shared: their partial (m, l, O) go to the workspace, and the CTA that
+// arrives last at a unit joins them, in CTA order (the result does not depend
+// on which CTA that is).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "hadq_attn.cuh"
+#include "hadq_common.cuh"
+#include "hadq_paged.cuh"
+
+namespace hadq {
+
+struct PagedAttnArgs {
+  const uint16_t* q;       // [rows][nqh][128] bf16 at a row stride
+  int64_t q_stride;
+  int64_t q_rows;
+  const int8_t* signs;     // [128] or NULL
+  const uint8_t* k_codes;  // [n_pages][nkv][page][16 * BITS]
+  const uint8_t* v_codes;
+  const float* k_scales;   // [n_pages][nkv][page][NG]
+  const float* v_scales;
+  const int32_t* table;    // [batch][max_pages]
+  const int32_t* lens;     // [batch]
+  const int32_t* cu;       // [batch + 1]
+  uint16_t* out;           // [rows][nqh][128] bf16
+  float* part_o;
+  float* part_ml;
+  unsigned* counters;      // zero before and after every call
+  int batch, nqh, nkv, g, page_log2, max_pages, n_pages;
+  int causal, window, sinks;
+  int row_lo, row_hi;      // this launch serves requests with row_lo < n * g <= row_hi
+  int min_tiles;           // fewest key tiles a CTA takes
+  float qmul;              // softmax scale * log2(e) / sqrt(128)
+  float inv_sqrt_dim;      // 1 / sqrt(128)
+};
+
+struct PagedReq {
+  int row0, n, len;  // first query row, query tokens, cached tokens
+  int rows;          // query rows per KV head that this launch serves (0: another launch's)
+};
+__device__ __forceinline__ PagedReq paged_req(const PagedAttnArgs& a, int b) {
+  PagedReq r;
+  r.row0 = a.cu[b];
+  const int64_t n = int64_t(a.cu[b + 1]) - r.row0;
+  // rows outside q are never touched, whatever cu holds
+  r.n = r.row0 < 0 || n <= 0 || r.row0 + n > a.q_rows ? 0 : int(n);
+  const int64_t room = int64_t(a.max_pages) << a.page_log2;
+  r.len = int(min(int64_t(max(a.lens[b], 0)), room));
+  const int rows = r.n * a.g;
+  r.rows = rows > a.row_lo && rows <= a.row_hi ? rows : 0;
+  return r;
+}
+
+// The key tiles (TILE tokens) that a group of query tokens first .. last sees:
+// [0, head) and [from, head-less end), listed one after the other.
+struct PagedTiles {
+  int head, from, count;  // tile index i < head: tile i; else tile i - head + from
+  int kv_end;             // keys at or past this are seen by none of the group
+};
+template <int TILE>
+__device__ __forceinline__ PagedTiles paged_tiles(const PagedAttnArgs& a, const PagedReq& r, int first, int last) {
+  PagedTiles t;
+  const int off = r.len - r.n;
+  t.kv_end = a.causal ? min(r.len, max(0, off + last + 1)) : r.len;
+  const int beg = a.window > 0 ? max(0, off + first - a.window + 1) : 0;
+  t.head = (min(min(a.sinks, beg), t.kv_end) + TILE - 1) / TILE;
+  t.from = max(beg / TILE, t.head);
+  t.count = max(1, t.head + max(0, (t.kv_end + TILE - 1) / TILE - t.from));
+  return t;
+}
+
+// Inclusive scan over the block; `part` has one entry per warp and may be
+// reused after the next barrier.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int nwarps, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) part[w] = v;
+  __syncthreads();
+  int64_t sum = 0, before = 0;
+  for (int i = 0; i < nwarps; ++i) {
+    if (i < w) before += part[i];
+    sum += part[i];
+  }
+  *total = sum;
+  return v + before;
+}
+
+// Where a CTA's piece of the line begins, and how the line is cut.
+struct PagedPiece {
+  int64_t quota;       // tiles per CTA
+  int64_t at, end;     // this CTA's tiles [at, end)
+  int b;               // request of the first one
+  int64_t in_request;  // its index within the request
+};
+struct PagedPlanSmem {
+  int64_t part[32];
+  int64_t at;
+  int b;
+};
+// tiles_of(b): the request's tiles over all heads and row groups.
+template <typename F>
+__device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPlanSmem& sm, F tiles_of) {
+  const int nt = blockDim.x, nwarps = nt >> 5;
+  PagedPiece p;
+  int64_t total = 0, own = 0, inc = 0;
+  for (int base = 0; base < a.batch; base += nt) {
+    const int b = base + int(threadIdx.x);
+    own = b < a.batch ? tiles_of(b) : 0;
+    int64_t sum;
+    inc = block_scan(own, sm.part, nwarps, &sum);
+    total += sum;
+  }
+  p.quota = max(int64_t(a.min_tiles), (total + gridDim.x - 1) / int64_t(gridDim.x));
+  p.at = int64_t(blockIdx.x) * p.quota;
+  p.end = min(total, p.at + p.quota);
+  p.b = 0;
+  p.in_request = 0;
+  if (p.at >= p.end) return p;  // uniform over the block
+  int64_t before = 0;
+  for (int base = 0; base < a.batch; base += nt) {
+    const int b = base + int(threadIdx.x);
+    int64_t sum = total;
+    if (a.batch > nt) {  // one chunk: the scan above is still in registers
+      own = b < a.batch ? tiles_of(b) : 0;
+      inc = block_scan(own, sm.part, nwarps, &sum);
+    }
+    const int64_t lo = before + inc - own;
+    if (own > 0 && p.at >= lo && p.at < lo + own) {
+      sm.b = b;
+      sm.at = p.at - lo;
+    }
+    before += sum;
+    if (before > p.at) break;
+  }
+  __syncthreads();
+  p.b = sm.b;
+  p.in_request = sm.at;
+  return p;
+}
+
+// ------------------------------------------------------- few query rows
+//
+// One pass over a unit's keys for 8 * RG query rows (RG = 1 or 2).  A warp
+// takes 16 keys at a time through its own cp.async ring:
+//  * scores by m16n8k32 s8 products: A = the query cut into two signed 8-bit
+//    digits of a 16-bit fixed-point number (row r: high digits, row r + 8: low
+//    digits), B = the key codes.  The integer sums are exact, and a lane's
+//    accumulators hold both digits of one row against its own keys;
+//  * the weights as a transposed product O^T += V^T P^T, m16n8k16 f16: A =
+//    value codes, exact in f16 (times the ratio of a group's scale to the
+//    row's largest, for groups below 128), B = the weights, which the lane
+//    already holds where this operand wants them.  No shuffle but the two of
+//    the row maximum.
+// A weight enters as f16 times its value row's scale over 2^e, e the exponent
+// of the largest value scale among the 16 keys, and the running reference
+// counts e in: m = max(score + e), so an f16 weight is at most 2^9 whatever
+// the scales are (11 bits kept, against the 8 of the bf16 output); l and O are
+// float32.
+//
+// Bound by HBM for long INT8 caches and close to the issue rate for INT4: a
+// cached row pair is 2 * (16 BITS + 512 / G) bytes against about 11 warp
+// instructions.
+constexpr int kPdThreads = 128;
+constexpr int kPdWarps = 4;
+constexpr int kPdTile = 64;  // keys per CTA step, 16 per warp
+constexpr int kPdPitch = kPagedDim + 4;
+
+__host__ __device__ constexpr int pd_stages(int bits) { return bits == 8 ? 3 : 4; }
+
+template <int RG, int NG, int BITS>
+struct __align__(16) PdSmem {
+  union {
+    uint8_t stage[kPdWarps][pd_stages(BITS)][attn_stage_bytes(NG, BITS)];
+    float comb[kPdWarps][8 * RG][kPdPitch];
+  } u;
+  int8_t qd[2][8 * RG][kPagedDim];  // query digits: high, low
+  float qscale[8 * RG];
+  float m[kPdWarps][8 * RG], l[kPdWarps][8 * RG];
+  PagedPlanSmem plan;
+  int last;
+};
+
+// 4 nibbles of two tokens (a: low half, b: high half of x) -> f16 pairs.
+__device__ __forceinline__ void i4x4_to_f16_tokens(uint32_t x, uint32_t (&r)[4]) {
+  // 1024 + (code + 8), or 1024 + 16 (code + 8) for the odd nibbles, whose
+  // sixteenth is 72 + code
+  const uint32_t y = x >> 8;
+  const uint32_t t0 = (x & 0x000F000Fu) ^ 0x64086408u, t1 = (x & 0x00F000F0u) ^ 0x64806480u;
+  const uint32_t t2 = (y & 0x000F000Fu) ^ 0x64086408u, t3 = (y & 0x00F000F0u) ^ 0x64806480u;
+  r[0] = f16x2_sub(t0, 0x64086408u);
+  r[2] = f16x2_sub(t2, 0x64086408u);
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(t1), "r"(0x2C002C00u), "r"(0xD480D480u));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(t3), "r"(0x2C002C00u), "r"(0xD480D480u));
+}
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A scale as the kernels use it: one that is not finite counts as zero, so
+// that a key nobody sees cannot reach a sum.
+__device__ __forceinline__ float clean_scale(float s) { return fabsf(s) < INFINITY ? s : 0.f; }
+
+// H_128 over idx = 4 * lane + r (bits 0-1 in registers, 2-6 on the lanes).
+__device__ __forceinline__ void warp_h128(float (&y)[4], int lane) {
+  bfly(y[0], y[1]);
+  bfly(y[2], y[3]);
+  bfly(y[0], y[2]);
+  bfly(y[1], y[3]);
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float s = (lane & m) ? -1.f : 1.f;
+    lane_stage<4>(y, m, s);
+  }
+}
+
+// One finished output row: rotate back, normalise, sign, store.  The lane's
+// y[r] is index 4 * lane + r of the order idx = 8 (dim & 15) + (dim >> 4).
+__device__ __forceinline__ void pd_finish(const PagedAttnArgs& a, float4 acc, float L, uint16_t* row, int lane) {
+  float y[4] = {acc.x, acc.y, acc.z, acc.w};
+  warp_h128(y, lane);
+  const float inv = L > 0.f ? a.inv_sqrt_dim / L : 0.f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int dim = 64 * (lane & 1) + 16 * r + (lane >> 1);
+    float v = y[r] * inv;
+    if (a.signs && a.signs[dim] < 0) v = -v;
+    row[dim] = uint16_t(pack_bf16x2(v, 0.f));
+  }
+}
+
+template <int RG, int NG, int BITS>
+__global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kernel(const PagedAttnArgs a) {
+  using RW = AttnRows<BITS>;
+  constexpr int KROW = RW::KROW, KP = RW::KP, VROW = RW::VROW, STV = RW::STV, STS = RW::STS;
+  constexpr int SB = attn_stage_bytes(NG, BITS);
+  constexpr int STAGES = pd_stages(BITS);
+  constexpr int ROWS = 8 * RG;
+  extern __shared__ __align__(16) uint8_t pd_smem_raw[];
+  PdSmem<RG, NG, BITS>& sm = *reinterpret_cast<PdSmem<RG, NG, BITS>*>(pd_smem_raw);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+
+  auto group_tiles = [&](const PagedReq& r, int rg) {
+    const int f = rg * ROWS, l = min(r.rows, f + ROWS) - 1;
+    return paged_tiles<kPdTile>(a, r, f / a.g, l / a.g);
+  };
+  auto head_tiles = [&](const PagedReq& r) {
+    int64_t s = 0;
+    for (int rg = 0; rg * ROWS < r.rows; ++rg) s += group_tiles(r, rg).count;
+    return s;
+  };
+  PagedPiece pc = paged_plan(a, sm.plan, [&](int b) { return head_tiles(paged_req(a, b)) * a.nkv; });
+  if (pc.at >= pc.end) return;
+
+  // first unit
+  int b = pc.b;
+  PagedReq rq = paged_req(a, b);
+  int h, rg = 0;
+  int64_t u;  // tile within the unit
+  {
+    const int64_t per = head_tiles(rq);
+    h = int(pc.in_request / per);
+    u = pc.in_request - h * per;
+    for (;;) {
+      const int c = group_tiles(rq, rg).count;
+      if (u < c) break;
+      u -= c;
+      ++rg;
+    }
+  }
+
+  const int cta = blockIdx.x;
+  int64_t at = pc.at;
+  while (at < pc.end) {
+    const PagedTiles tl = group_tiles(rq, rg);
+    const int i0 = int(u), i1 = int(min(int64_t(tl.count), u + (pc.end - at)));
+    const int64_t ustart = at - u;
+    const int nw = i1 - i0;
+    const int row_base = rg * ROWS;
+    const int nrows = min(ROWS, rq.rows - row_base);
+    const int off = rq.len - rq.n;
+
+    // ---- queries: rotate, cut into digits ----
+    for (int r = w; r < ROWS; r += kPdWarps) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < nrows) {
+        const int tok = (row_base + r) / a.g, hh = (row_base + r) - tok * a.g;
+        const uint2 raw = *reinterpret_cast<const uint2*>(a.q + int64_t(rq.row0 + tok) * a.q_stride +
+                                                          int64_t(h * a.g + hh) * kPagedDim + 4 * lane);
+        x[0] = bf16lo(raw.x);
+        x[1] = bf16hi(raw.x);
+        x[2] = bf16lo(raw.y);
+        x[3] = bf16hi(raw.y);
+        if (a.signs) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (a.signs[4 * lane + i] < 0) x[i] = -x[i];
+        }
+      }
+      warp_h128(x, lane);
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] *= a.qmul;
+        amax = fmaxf(amax, fabsf(x[i]));
+      }
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      // 32000 steps to the largest entry: an error of 2^-16 of it per entry.
+      // Below 2^-100 a query counts as zero.
+      const bool zero = !(amax >= 7.888609e-31f);
+      const float up = zero ? 0.f : 32000.f / amax;
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int qf = __float2int_rn(x[i] * up);
+        const int e1 = (qf + 128) >> 8;
+        hi |= uint32_t(e1 & 0xff) << (8 * i);
+        lo |= uint32_t((qf - 256 * e1) & 0xff) << (8 * i);
+      }
+      *reinterpret_cast<uint32_t*>(&sm.qd[0][r][4 * lane]) = hi;
+      *reinterpret_cast<uint32_t*>(&sm.qd[1][r][4 * lane]) = lo;
+      if (lane == 0) sm.qscale[r] = zero ? 0.f : amax * (BITS == 4 ? 1.f / (16.f * 32000.f) : 1.f / 32000.f);
+    }
+    __syncthreads();
+
+    uint32_t qa[RG][4][4];
+    float qs[RG];
+    int lim[RG], low[RG];  // row g sees keys below lim, of these those from low on or below sinks
+#pragma unroll
+    for (int k = 0; k < RG; ++k) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int d0 = NG == 1 ? 32 * j + 8 * s : 32 * s + 8 * j;  // this lane's 8 dims of k-step s
+        const uint2 r0 = *reinterpret_cast<const uint2*>(&sm.qd[0][8 * k + g][d0]);
+        const uint2 r1 = *reinterpret_cast<const uint2*>(&sm.qd[1][8 * k + g][d0]);
+        qa[k][s][0] = __byte_perm(r0.x, r0.y, 0x6420);
+        qa[k][s][1] = __byte_perm(r1.x, r1.y, 0x6420);
+        qa[k][s][2] = __byte_perm(r0.x, r0.y, 0x7531);
+        qa[k][s][3] = __byte_perm(r1.x, r1.y, 0x7531);
+      }
+      qs[k] = sm.qscale[8 * k + g];
+      const int tok = min(row_base + 8 * k + g, rq.rows - 1) / a.g;
+      lim[k] = a.causal ? min(rq.len, off + tok + 1) : rq.len;
+      low[k] = a.window > 0 ? off + tok - a.window + 1 : 0;
+    }
+    // keys that every row of the unit sees need no mask: those below all_lim
+    // and, with a window, from all_low on
+    const int f_tok = row_base / a.g, l_tok = (row_base + nrows - 1) / a.g;
+    const int all_lim = a.causal ? off + f_tok + 1 : rq.len;
+    const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
+
+    // ---- this warp's ring ----
+    auto key0 = [&](int k) {  // first of this warp's 16 keys in step k
+      const int i = i0 + k;
+      return (i < tl.head ? i : i - tl.head + tl.from) * kPdTile + 16 * w;
+    };
+    const int32_t* tab = a.table + int64_t(b) * a.max_pages;
+    auto page_of = [&](int k) {  // page of step k's keys, -1: none of them is cached
+      if (k >= nw) return -1;
+      const int t = key0(k);
+      if (t >= tl.kv_end) return -1;
+      const int p = __ldg(tab + (t >> a.page_log2));
+      return unsigned(p) < unsigned(a.n_pages) ? p : -1;
+    };
+    constexpr int CPR = KROW / 16, TPP = 32 / CPR, NPASS = 16 / TPP;
+    const int ctok = lane / CPR, cpart = lane % CPR;
+    const uint32_t s_ring = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.u.stage[w][0][0]));
+    const uint32_t d_k = ctok * KP + cpart * 16, d_v = STV + ctok * VROW + cpart * 16;
+    const int src0 = ctok * KROW + cpart * 16;
+    uint32_t okbits = 0;  // bit (step % 8): the step's keys are in the ring
+    auto issue = [&](int k, int page) {
+      okbits &= ~(1u << (k & 7));
+      if (page >= 0) {
+        okbits |= 1u << (k & 7);
+        const int64_t row = ((int64_t(page) * a.nkv + h) << a.page_log2) + (key0(k) & ((1 << a.page_log2) - 1));
+        const uint32_t st = s_ring + uint32_t(k % STAGES) * SB;
+        const uint8_t* gk = a.k_codes + row * KROW + src0;
+        const uint8_t* gv = a.v_codes + row * KROW + src0;
+#pragma unroll
+        for (int p = 0; p < NPASS; ++p) {
+          cp_async16(st + d_k + TPP * p * KP, gk + TPP * p * KROW);
+          cp_async16(st + d_v + TPP * p * VROW, gv + TPP * p * KROW);
+        }
+        if (lane < 8 * NG) {  // 4 NG pieces of 16 bytes of K scales, then as many of V
+          const float* gs = (lane < 4 * NG ? a.k_scales : a.v_scales) + row * NG + 4 * (lane % (4 * NG));
+          cp_async16(st + STS + 16 * lane, gs);
+        }
+      }
+      cp_async_commit();
+    };
+
+    float o[RG][8][4];
+    float m_run[RG], l_run[RG];
+#pragma unroll
+    for (int k = 0; k < RG; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[k][i][0] = o[k][i][1] = o[k][i][2] = o[k][i][3] = 0.f;
+      m_run[k] = -INFINITY;
+      l_run[k] = 0.f;
+    }
+    {
+      int pg[STAGES - 1];
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) pg[k] = page_of(k);
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) issue(k, pg[k]);
+    }
+    int pg_next = page_of(STAGES - 1);
+
+    for (int k = 0; k < nw; ++k) {
+      issue(k + STAGES - 1, pg_next);
+      pg_next = page_of(k + STAGES);
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      if ((okbits >> (k & 7)) & 1u) {
+        const uint8_t* st = sm.u.stage[w][k % STAGES];
+        const float* sc = reinterpret_cast<const float*>(st + STS);  // [16][NG] K, then [16][NG] V
+        const int t0 = key0(k);
+
+        // exponent of the largest value scale among the 16 keys
+        float vmax = 0.f;
+#pragma unroll
+        for (int q = 0; q < (NG + 1) / 2; ++q) vmax = fmaxf(vmax, clean_scale(sc[16 * NG + 32 * q + (NG == 1 ? lane & 15 : lane)]));
+        const int ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)) >> 23), 27), 227);
+        const float vdown = __uint_as_float(uint32_t(254 - ve) << 23);  // 2^-e
+        const float vexp = float(ve - 127);                             // e
+
+        // ---- scores of 8 RG rows x 16 keys ----
+        int c[RG][2][NG][4];
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+#pragma unroll
+          for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[r][0][q][i] = c[r][1][q][i] = 0;
+        if constexpr (BITS == 4) {
+          uint32_t kw[2][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* kr = st + (g + 8 * x) * KP;
+            if constexpr (NG == 1) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kr + 16 * j);
+              kw[x][0] = v.x; kw[x][1] = v.y; kw[x][2] = v.z; kw[x][3] = v.w;
+            } else {
+#pragma unroll
+              for (int s = 0; s < 4; ++s) kw[x][s] = *reinterpret_cast<const uint32_t*>(kr + 16 * s + 4 * j);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t e, od;
+              int4x8_to_s8x16(kw[x][s], e, od);
+#pragma unroll
+              for (int r = 0; r < RG; ++r) mma_s8_16832(c[r][x][s * NG / 4], qa[r][s], e, od);
+            }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* kr = st + (g + 8 * x) * KP;
+            uint2 kw[4];
+            if constexpr (NG == 1) {
+              const uint4 v0 = *reinterpret_cast<const uint4*>(kr + 32 * j);
+              const uint4 v1 = *reinterpret_cast<const uint4*>(kr + 32 * j + 16);
+              kw[0] = make_uint2(v0.x, v0.y); kw[1] = make_uint2(v0.z, v0.w);
+              kw[2] = make_uint2(v1.x, v1.y); kw[3] = make_uint2(v1.z, v1.w);
+            } else {
+#pragma unroll
+              for (int s = 0; s < 4; ++s) kw[s] = *reinterpret_cast<const uint2*>(kr + 32 * s + 8 * j);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t e = __byte_perm(kw[s].x, kw[s].y, 0x6420), od = __byte_perm(kw[s].x, kw[s].y, 0x7531);
+#pragma unroll
+              for (int r = 0; r < RG; ++r) mma_s8_16832(c[r][x][s * NG / 4], qa[r][s], e, od);
+            }
+          }
+        }
+
+        // this lane's keys: 2j, 2j + 1 (x = 0) and 2j + 8, 2j + 9 (x = 1)
+        float kscl[2][2][NG];
+        float pvs[2][2];   // value scale (the row's largest) over 2^e
+        float ratio[2][2]; // groups: this lane's group of value dims over the row's largest
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int t = 2 * j + 8 * x + y;
+#pragma unroll
+            for (int q = 0; q < NG; ++q) kscl[x][y][q] = sc[t * NG + q];
+            float top = 0.f;
+#pragma unroll
+            for (int q = 0; q < NG; ++q) top = fmaxf(top, clean_scale(sc[(16 + t) * NG + q]));
+            pvs[x][y] = top * vdown;
+            ratio[x][y] = 0.f;
+            if constexpr (NG > 1) ratio[x][y] = top > 0.f ? clean_scale(sc[(16 + t) * NG + (g * NG >> 3)]) / top : 0.f;
+          }
+
+        const bool masked = t0 + 16 > all_lim || (a.window > 0 && t0 < all_low);
+        uint32_t pb[RG][2];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          float s[2][2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float v = 0.f;
+#pragma unroll
+              for (int q = 0; q < NG; ++q) {
+                const float p = float(c[r][x][q][y] * 256 + c[r][x][q][2 + y]);
+                v = NG == 1 ? p * kscl[x][y][q] : fmaf(p, kscl[x][y][q], v);
+              }
+              s[x][y] = v * qs[r];
+            }
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int t = t0 + 2 * j + 8 * x + y;
+                if (t >= lim[r] || (a.window > 0 && t < low[r] && t >= a.sinks)) s[x][y] = -INFINITY;
+              }
+          }
+          float top = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) + vexp;
+          // the reference rises only when the tile's maximum exceeds it by
+          // more than kAttnSlack, so weights stay below 2^8
+          const bool need = top > m_run[r] + kAttnSlack;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? exp2f(m_run[r] - top) : 1.f;
+            if (need) m_run[r] = top;
+            l_run[r] *= alpha;
+            // accumulators of this lane belong to rows 2j, 2j + 1
+            const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * j), a1 = __shfl_sync(0xffffffffu, alpha, 8 * j + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[r][i][0] *= a0;
+              o[r][i][1] *= a1;
+              o[r][i][2] *= a0;
+              o[r][i][3] *= a1;
+            }
+          }
+          const float sub = m_run[r] == -INFINITY ? 0.f : vexp - m_run[r];
+          const float p00 = exp2_ftz(s[0][0] + sub), p01 = exp2_ftz(s[0][1] + sub);
+          const float p10 = exp2_ftz(s[1][0] + sub), p11 = exp2_ftz(s[1][1] + sub);
+          l_run[r] = fmaf((p00 + p01) + (p10 + p11), vdown, l_run[r]);
+          pb[r][0] = cvt_f16x2(p00 * pvs[0][0], p01 * pvs[0][1]);
+          pb[r][1] = cvt_f16x2(p10 * pvs[1][0], p11 * pvs[1][1]);
+        }
+
+        // ---- O^T += V^T P^T; the lane's value dims are 16 g + d, d = 0..15 ----
+        uint32_t r_ab = 0, r_cd = 0;
+        if constexpr (NG > 1) {
+          r_ab = cvt_f16x2(ratio[0][0], ratio[0][1]);
+          r_cd = cvt_f16x2(ratio[1][0], ratio[1][1]);
+        }
+        auto pv = [&](int i, uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {  // dims 2i, 2i + 1
+          if constexpr (NG > 1) {
+            x0 = f16x2_mul(x0, r_ab);
+            x1 = f16x2_mul(x1, r_ab);
+            y0 = f16x2_mul(y0, r_cd);
+            y1 = f16x2_mul(y1, r_cd);
+          }
+#pragma unroll
+          for (int r = 0; r < RG; ++r) mma_h16_f16(o[r][i], x0, x1, y0, y1, pb[r][0], pb[r][1]);
+        };
+        if constexpr (BITS == 4) {
+          const uint8_t* vr = st + STV + 8 * g;
+          const uint2 va = *reinterpret_cast<const uint2*>(vr + (2 * j) * VROW);
+          const uint2 vb = *reinterpret_cast<const uint2*>(vr + (2 * j + 1) * VROW);
+          const uint2 vc = *reinterpret_cast<const uint2*>(vr + (2 * j + 8) * VROW);
+          const uint2 vd = *reinterpret_cast<const uint2*>(vr + (2 * j + 9) * VROW);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
+            uint32_t x[4], y[4];
+            i4x4_to_f16_tokens(__byte_perm(q < 2 ? va.x : va.y, q < 2 ? vb.x : vb.y, sel), x);
+            i4x4_to_f16_tokens(__byte_perm(q < 2 ? vc.x : vc.y, q < 2 ? vd.x : vd.y, sel), y);
+            pv(2 * q, x[0], x[1], y[0], y[1]);
+            pv(2 * q + 1, x[2], x[3], y[2], y[3]);
+          }
+        } else {
+          const uint8_t* vr = st + STV + 16 * g;
+          const uint4 va = *reinterpret_cast<const uint4*>(vr + (2 * j) * VROW);
+          const uint4 vb = *reinterpret_cast<const uint4*>(vr + (2 * j + 1) * VROW);
+          const uint4 vc = *reinterpret_cast<const uint4*>(vr + (2 * j + 8) * VROW);
+          const uint4 vd = *reinterpret_cast<const uint4*>(vr + (2 * j + 9) * VROW);
+          const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+          const uint32_t wc[4] = {vc.x, vc.y, vc.z, vc.w}, wd[4] = {vd.x, vd.y, vd.z, vd.w};
+          auto two = [](uint32_t p, uint32_t q, uint32_t sel) {
+            return f16x2_sub((__byte_perm(p, q, sel) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          };
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            pv(2 * q, two(wa[q], wb[q], 0x0400), two(wa[q], wb[q], 0x0501), two(wc[q], wd[q], 0x0400), two(wc[q], wd[q], 0x0501));
+            pv(2 * q + 1, two(wa[q], wb[q], 0x0602), two(wa[q], wb[q], 0x0703), two(wc[q], wd[q], 0x0602), two(wc[q], wd[q], 0x0703));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its ring: the merge area reuses it
+
+    // ---- join the four warps ----
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+      if (j == 0) {
+        sm.m[w][8 * r + g] = m_run[r];
+        sm.l[w][8 * r + g] = l_run[r];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // dims 16 g + 2 i, + 1 of rows 2j, 2j + 1; idx = 8 (dim & 15) + (dim >> 4)
+        sm.u.comb[w][8 * r + 2 * j][16 * i + g] = o[r][i][0];
+        sm.u.comb[w][8 * r + 2 * j + 1][16 * i + g] = o[r][i][1];
+        sm.u.comb[w][8 * r + 2 * j][16 * i + 8 + g] = o[r][i][2];
+        sm.u.comb[w][8 * r + 2 * j + 1][16 * i + 8 + g] = o[r][i][3];
+      }
+    }
+    __syncthreads();
+    const bool whole = i0 == 0 && i1 == tl.count;
+    const int64_t slot = (2 * int64_t(cta) + (u == 0 ? 1 : 0)) * ROWS;
+    auto out_row = [&](int r) {
+      const int tok = (row_base + r) / a.g, hh = (row_base + r) - tok * a.g;
+      return a.out + (int64_t(rq.row0 + tok) * a.nqh + h * a.g + hh) * kPagedDim;
+    };
+    for (int r = w; r < nrows; r += kPdWarps) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int x = 0; x < kPdWarps; ++x) M = fmaxf(M, sm.m[x][r]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kPdWarps; ++x) {
+        const float f = sm.m[x][r] == -INFINITY ? 0.f : exp2f(sm.m[x][r] - M);
+        L = fmaf(f, sm.l[x][r], L);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.u.comb[x][r][4 * lane]);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (whole) {
+        pd_finish(a, acc, L, out_row(r), lane);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot + r) * kPagedDim + 4 * lane) = acc;
+        if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + (slot + r) * 2) = make_float2(M, L);
+      }
+    }
+    if (!whole) {
+      const int c0 = int(ustart / pc.quota), c1 = int((ustart + tl.count - 1) / pc.quota);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sm.last = atomicAdd(a.counters + c0, 1u) == unsigned(c1 - c0);
+      __syncthreads();
+      if (sm.last) {
+        __threadfence();
+        // CTA c0 began the unit (its second slot); the others carry it on (their first)
+        for (int r = w; r < nrows; r += kPdWarps) {
+          auto at_of = [&](int x) { return (2 * int64_t(x) + (x == c0 ? 1 : 0)) * ROWS + r; };
+          float M = -INFINITY;
+          for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(a.part_ml + at_of(x) * 2));
+#pragma unroll
+          for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+          float L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int base = c0; base <= c1; base += 32) {
+            float f = 0.f;
+            if (base + lane <= c1) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at_of(base + lane) * 2));
+              f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+              L = fmaf(f, ml.y, L);
+            }
+            const int n = min(32, c1 - base + 1);
+            for (int x = 0; x < n; x += 8) {
+              float4 v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                if (x + y < n) v[y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at_of(base + x + y) * kPagedDim) + lane);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const float fy = __shfl_sync(0xffffffffu, f, x + y);
+                if (x + y < n) {
+                  acc.x = fmaf(fy, v[y].x, acc.x);
+                  acc.y = fmaf(fy, v[y].y, acc.y);
+                  acc.z = fmaf(fy, v[y].z, acc.z);
+                  acc.w = fmaf(fy, v[y].w, acc.w);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+          pd_finish(a, acc, L, out_row(r), lane);
+        }
+        if (tid == 0) a.counters[c0] = 0u;  // ready for the next call
+      }
+    }
+    __syncthreads();  // the merge area becomes the next unit's ring
+
+    // ---- next unit ----
+    at += i1 - i0;
+    u = 0;
+    if (at < pc.end) {
+      ++rg;
+      if (rg * ROWS >= rq.rows) {
+        rg = 0;
+        if (++h == a.nkv) {
+          h = 0;
+          do {
+            rq = paged_req(a, ++b);
+          } while (rq.rows == 0);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace hadq

@@ -400,6 +400,150 @@ hadq_status hadq_kv_decode_attention_noalloc(const void *q, const void *k_codes,
                                              hadq_out_dtype out_dtype, hadq_stream_t stream);
 
 /*
+ * The paged KV cache.  A request's cached tokens live in pages of page_size
+ * tokens (a power of two, 16 .. 1024) anywhere in a pool of n_pages pages.
+ * One tensor (K or V) of the pool is
+ *   codes   [n_pages, n_kv_heads, page_size, dim/2] bytes of packed INT4, or
+ *           [..., dim] int8 for bits 8; 16-byte aligned,
+ *   scales  float32 [n_pages, n_kv_heads, page_size, dim/group],
+ * every row what hadq_rotate_quantize writes for dim 128, block 128 (or -1),
+ * group 128 (or -1), 64 or 32 and bits 4 or 8; other valid combinations return
+ * HADQ_ERR_UNSUPPORTED, as does a pool of 2^31 tokens or more.  A slot is
+ * page * page_size + offset; a block table is int32 [batch, max_pages], entry
+ * (b, p) the page of request b's tokens p * page_size and on.
+ * A serving step: hadq_paged_slots once, then for every layer
+ * hadq_paged_append and hadq_paged_attention.  Lengths, tables and slots are
+ * read on the device only, so the calls can be captured into a CUDA graph and
+ * replayed with other lengths.
+ */
+
+/*
+ * hadq_paged_slots -- block tables and slots of the tokens that join the
+ * cache, from the requests' lengths.  Request b holds cached_lens[b] tokens
+ * (its first ceil(cached / page_size) table entries name their pages) and gets
+ * new_lens[b] more (negative lengths count as 0).  Requests take pages from
+ * free_pages in order, request 0 first.
+ *
+ *   cached_lens, new_lens  device int32 [batch], batch at most 16384
+ *                (HADQ_ERR_UNSUPPORTED beyond).
+ *   free_pages   device int32 [n_free], the pages that may be taken.
+ *   block_table  device int32 [batch, max_pages]; the entries of new pages are
+ *                written, all others are left as they were.
+ *   total_lens   device output int32 [batch]: cached + new.  A request whose
+ *                pages the free list or the table has no room for is refused:
+ *                its total is 0, its slots are -1 and its table is left as it
+ *                was (and so are later requests that need a page, once the
+ *                free list has run out).  Not one of the input arrays.
+ *   cu_new       device output int32 [batch + 1]: row of each request's first
+ *                new token in the packed rows of new tokens (q, k, v), and
+ *                their number (the new tokens together are below 2^31).
+ *   slots        device output int32 [capacity]: slot of every packed row; -1
+ *                behind the last one, so that capacity may exceed their
+ *                number.  Rows at or past capacity get no slot.
+ *   counts       device output int32 [2]: pages taken (the first so many of
+ *                free_pages), requests refused.
+ */
+hadq_status hadq_paged_slots(const int32_t *cached_lens, const int32_t *new_lens, int32_t batch,
+                             const int32_t *free_pages, int32_t n_free, int32_t page_size,
+                             int32_t *block_table, int32_t max_pages, int32_t *total_lens,
+                             int32_t *cu_new, int32_t *slots, int64_t capacity, int32_t *counts,
+                             hadq_stream_t stream);
+
+/*
+ * hadq_paged_append -- hadq_rotate_quantize of the K and V rows of new tokens,
+ * written to the tokens' slots, in one launch.
+ *
+ *   k, v      device bf16 [tokens, n_kv_heads, dim] with k_stride (v_stride)
+ *             elements from one token to the next, at least n_kv_heads * dim
+ *             and a multiple of 8; 16-byte aligned.
+ *   slots     device int32 [tokens]; a token whose slot is outside the pool is
+ *             skipped.  Two tokens on one slot leave either of them there.
+ *   k_codes, k_scales, v_codes, v_scales  the pool; rows of other slots are
+ *             left as they were.
+ *   signs     device int8 [dim] or NULL.
+ */
+hadq_status hadq_paged_append(const void *k, const void *v, int64_t tokens, int64_t k_stride,
+                              int64_t v_stride, int32_t n_kv_heads, int32_t dim, int32_t block,
+                              const int8_t *signs, int32_t bits, int32_t group, const int32_t *slots,
+                              void *k_codes, float *k_scales, void *v_codes, float *v_scales,
+                              int64_t n_pages, int32_t page_size, hadq_stream_t stream);
+
+/*
+ * hadq_paged_gather -- hadq_dequant_rotate_inv of the rows of one pool tensor
+ * at the given slots.
+ *
+ *   out       device output [tokens, n_kv_heads, dim], bf16 or float32 (by
+ *             out_dtype), 16-byte aligned; the row of a token whose slot is
+ *             outside the pool is left as it was.
+ *   Other arguments as for hadq_paged_append.
+ */
+hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_pages,
+                              int32_t page_size, int32_t n_kv_heads, int32_t dim, int32_t block,
+                              const int8_t *signs, int32_t bits, int32_t group, const int32_t *slots,
+                              int64_t tokens, void *out, hadq_out_dtype out_dtype, hadq_stream_t stream);
+
+/*
+ * hadq_paged_attention -- attention of each request's new tokens over its
+ * pages: single tokens (decoding), several (speculative tokens, prompt chunks)
+ * and, with causal 0, queries over the cached states of another sequence
+ * (cross attention).  The arithmetic is that of hadq_kv_decode_attention; the
+ * new tokens' own K and V are in the cache before the call.
+ *
+ *   q            device bf16 [q_rows, n_q_heads, dim] with q_stride elements
+ *                from one row to the next, at least n_q_heads * dim and a
+ *                multiple of 8; 16-byte aligned.  Query head h reads KV head
+ *                h / (n_q_heads / n_kv_heads).
+ *   cu_new       device int32 [batch + 1]: request b's queries are the rows
+ *                cu_new[b] .. cu_new[b + 1) - 1 (none, or a range outside q:
+ *                the request is passed over).  Rows of `out` behind the last
+ *                request are left as they were.
+ *   total_lens   device int32 [batch]: cached tokens, the new ones among them
+ *                when causal.
+ *   max_new      upper bound of the requests' query counts, known to the host:
+ *                it chooses the kernels and the workspace size, not the
+ *                result.
+ *   block_table  device int32 [batch, max_pages], max_pages * page_size at
+ *                most 2^30.  Keys on a page outside the pool are seen by
+ *                nobody.
+ *   causal       1: query i of a request with n queries and len cached tokens
+ *                is at position len - n + i and sees the keys up to its own;
+ *                0: every query sees all len keys.
+ *   window       0, or (causal) only the last `window` of those keys, its own
+ *                among them, and the first `sinks` ("Hartmann rotation,
+ *                lightweight QAT, streaming attention", section 3: head and
+ *                local window).
+ *   softmax_scale  > 0 and finite (usually 1/sqrt(dim)).
+ *   out          device output bf16 [q_rows, n_q_heads, dim], 16-byte aligned.
+ *                A query that sees no key gets zeros.
+ *   workspace    device scratch of at least hadq_paged_workspace_size() bytes,
+ *                256-byte aligned, zero-filled before its first use; every
+ *                call leaves it ready for the next.  Calls that share one must
+ *                be ordered (also two captured graphs that do).
+ *
+ * Softmax statistics and sums are float32; the rotated query enters the score
+ * product, and a weight the value product, with at least 11 significant bits.
+ * A scale that is not finite counts as zero.  Value scales below 2^-100 (and
+ * queries all of whose scaled rotated entries are) count as zero.
+ */
+hadq_status hadq_paged_attention(const void *q, int64_t q_rows, int64_t q_stride,
+                                 const int32_t *cu_new, const int32_t *total_lens, int32_t batch,
+                                 int32_t max_new, const void *k_codes, const float *k_scales,
+                                 const void *v_codes, const float *v_scales, int64_t n_pages,
+                                 int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                 int32_t n_q_heads, int32_t n_kv_heads, int32_t dim, int32_t block,
+                                 const int8_t *signs, int32_t bits, int32_t group, int32_t causal,
+                                 int32_t window, int32_t sinks, float softmax_scale, void *out,
+                                 void *workspace, size_t workspace_bytes, hadq_stream_t stream);
+
+/*
+ * hadq_paged_workspace_size -- host-only: bytes of workspace that
+ * hadq_paged_attention needs for these sizes on any device, whatever the batch
+ * and the lengths.
+ */
+hadq_status hadq_paged_workspace_size(int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                      size_t *bytes);
+
+/*
  * hadq_plan -- host-only: validate the sizes of a call and report the kernel
  * family it would use.  direction 0 = rotate_quantize, 1 = dequant_rotate_inv.
  * `aligned16` says whether every pointer of the call is 16-byte aligned.
