@@ -28,6 +28,7 @@
 #include "hadq_kron.cuh"
 #include "hadq_paged.cuh"
 #include "hadq_paged_attn.cuh"
+#include "hadq_paged_tc.cuh"
 #include "hadq_kernels.h"
 
 namespace {
@@ -1377,6 +1378,11 @@ constexpr int kPagedMaxCtas = 640;
 constexpr size_t kPagedCounterBytes = 8192;
 static size_t paged_part_bytes(int64_t ctas, int rows) { return size_t(ctas) * 2 * rows * (hadq::kPagedDim + 2) * sizeof(float); }
 
+// Requests of up to this many query rows per KV head go to the kernel for few
+// rows.
+constexpr int kPagedFewRows = 16;
+static bool paged_uses_chunk(int64_t max_rows, int g) { return max_rows > kPagedFewRows && g <= hadq::kPtRows; }
+
 static hadq_status paged_heads_check(int32_t max_new, int32_t nqh, int32_t nkv) {
   if (max_new < 0) return fail(HADQ_ERR_INVALID_ARG, "max_new must be >= 0 (got %d)", max_new);
   if (nqh < 1 || nkv < 1)
@@ -1390,7 +1396,9 @@ hadq_status hadq_paged_workspace_size(int32_t max_new, int32_t n_q_heads, int32_
   if (st != HADQ_OK) return st;
   if (!bytes) return fail(HADQ_ERR_INVALID_ARG, "bytes must not be NULL");
   const int64_t rows = int64_t(max_new) * (n_q_heads / n_kv_heads);
-  *bytes = kPagedCounterBytes + paged_part_bytes(kPagedMaxCtas, rows <= 8 ? 8 : 16);
+  const size_t few = paged_part_bytes(kPagedMaxCtas, rows <= 8 ? 8 : 16);
+  const size_t many = paged_uses_chunk(rows, n_q_heads / n_kv_heads) ? paged_part_bytes(hadq::kPtMaxCtas, hadq::kPtRows) : 0;
+  *bytes = kPagedCounterBytes + (few > many ? few : many);  // the two kernels run one after the other
   return HADQ_OK;
 }
 
@@ -1466,6 +1474,34 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes);
 
   const int64_t rows = int64_t(max_new) * a.g;
+  a.row_lo = 0;
+  a.row_hi = 0x7fffffff;
+  if (paged_uses_chunk(rows, a.g)) {
+    const void* fn = hadq::paged_chunk_kernel_ptr(p.ng, bits);
+    const size_t smem = hadq::paged_chunk_smem();
+    unsigned* fault = hadq::tc_fault_word();
+    if (!fault) return fail(HADQ_ERR_CUDA, "paged attention kernel: the fault word has no device address");
+    int res = 1;
+    st = prepare(fn, hadq::kPtThreads, smem, "paged attention kernel", &res);
+    if (st != HADQ_OK) return st;
+    const int64_t sms = sm_count(), grid = sms < hadq::kPtMaxCtas ? sms : hadq::kPtMaxCtas;
+    if (batch > 1) a.row_lo = kPagedFewRows;  // one request: this kernel alone takes it, whatever its rows
+    a.min_tiles = 1;
+    a.part_o = part;
+    a.part_ml = part + grid * 2 * hadq::kPtRows * hadq::kPagedDim;
+    void* argv[] = {&a, &fault};
+    const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned(grid)), dim3(hadq::kPtThreads), argv, smem,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      g_launches.fetch_add(1, std::memory_order_relaxed);
+      return fail(HADQ_ERR_CUDA, "paged attention kernel launch failed: %s", cudaGetErrorString(e));
+    }
+    st = after_launch("paged attention kernel");
+    if (st != HADQ_OK || batch == 1) return st;
+    a.row_lo = 0;
+    a.row_hi = kPagedFewRows;
+  }
   const int rg = rows <= 8 ? 1 : 2;
   size_t smem = 0;
   const void* fn = hadq::paged_decode_kernel_ptr(rg, p.ng, bits, &smem);
@@ -1474,8 +1510,6 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
   if (st != HADQ_OK) return st;
   int64_t grid = int64_t(res) * sm_count();
   if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
-  a.row_lo = 0;
-  a.row_hi = 0x7fffffff;
   a.min_tiles = 1;
   a.part_o = part;
   a.part_ml = part + grid * 2 * 8 * rg * hadq::kPagedDim;

@@ -78,5 +78,9 @@ const void* paged_gather_kernel_ptr(int bits, int ng, bool f32);
 // Attention over it for units of 8 * rg query rows (rg = 1, 2); writes the
 // dynamic shared memory it needs to *smem.
 const void* paged_decode_kernel_ptr(int rg, int ng, int bits, size_t* smem);
+// The same for units of 256 query rows, on tcgen05 tensor cores (kPtThreads
+// threads, one CTA per SM).
+const void* paged_chunk_kernel_ptr(int ng, int bits);
+size_t paged_chunk_smem();
 
 }  // namespace hadq
