@@ -397,63 +397,92 @@ def hadq_kv_decode_attention_noalloc(q: torch.Tensor, k_codes: torch.Tensor, k_s
 
 # ---------------------------------------------------------- paged KV cache
 
-def _on_device(t, name, dtype, device, shape=None):
-    """A contiguous tensor of this type on this device (and of this shape)."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        _need(t, name, dtype, device)
-    if shape is not None and tuple(t.shape) != shape:
+_U8, _I8, _I32, _F32, _BF16 = torch.uint8, torch.int8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _on(t, name, dtype, index, shape=None):
+    """A contiguous tensor of this type on CUDA device ``index`` (and of this shape)."""
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _need(t, name, dtype, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
-def _call(fn, device, stream, *args):
+def _call(fn, index, stream, *args):
     """Call a C entry point on the tensors' device: ``args`` and the stream
-    (its current stream when none is given)."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+    (that device's current stream when none is given)."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, index, stream, *args)
+    if stream is None:
+        stream = _raw_stream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = fn(*args, stream)
+    if st:
+        _check(st)
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without building a Stream object per call (1 us of a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _new(like, shape, dtype, stream, zero=False):
+    """A tensor of the stream that the call runs on (allocated, and zeroed, in its order)."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+        with torch.cuda.stream(stream):
+            return _new(like, shape, dtype, None, zero)
+    return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows_view(t, name, device, heads):
+def _rows_view(t, name, index, heads):
     """Row stride of a bf16 [tokens, heads, dim] tensor whose tokens are
     contiguous rows at any stride (a slice of a wider projection)."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, got {t.device}")
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, dim], got {list(t.shape)}")
     n, h, d = t.shape
-    if t.stride(2) != 1 and d > 1 or t.stride(1) != d and h > 1:
+    row, head, col = t.stride()
+    if col != 1 and d > 1 or head != d and h > 1:
         raise ValueError(f"{name} must hold each token's [heads, dim] contiguously")
-    return t.stride(0) if n > 1 else h * d
+    return row if n > 1 else h * d
 
 
-def _pool(codes, scales, name, device, bits, group, shape=None):
+def _pool(codes, scales, name, index, bits, group, shape=None):
     """Check one tensor of the pool; its [n_pages, n_kv_heads, page_size, bytes]."""
-    if codes.dim() != 4:
-        raise ValueError(f"{name}_codes must be [n_pages, n_kv_heads, page_size, dim*bits/8], got {list(codes.shape)}")
-    if codes.dtype is torch.int8:  # INT8 caches may come as int8
-        codes = codes.view(torch.uint8)
-    _on_device(codes, f"{name}_codes", torch.uint8, device, shape)
-    if codes.shape[3] != 16 * bits:
-        raise ValueError(f"{name}_codes rows hold {codes.shape[3]} bytes, expected 128*bits/8 = {16 * bits}")
-    _on_device(scales, f"{name}_scales", torch.float32, device)
+    got, sc = codes.shape, scales.shape
     per = 128 // group if group > 0 and 128 % group == 0 else 1
-    if scales.numel() != codes.shape[0] * codes.shape[1] * codes.shape[2] * per or scales.shape[:3] != codes.shape[:3]:
-        raise ValueError(f"{name}_scales must be [n_pages, n_kv_heads, page_size, dim/group], got {list(scales.shape)}")
-    return codes.shape
+    if ((codes.dtype is _U8 or codes.dtype is _I8) and scales.dtype is _F32  # INT8 caches may come as int8
+            and codes.get_device() == index == scales.get_device() and codes.is_contiguous() and scales.is_contiguous()
+            and len(got) == 4 and got[3] == 16 * bits and (shape is None or got == shape)
+            and sc[:3] == got[:3] and (sc[3:] == (per,) or (per == 1 and len(sc) == 3))):
+        return got
+    if codes.dim() != 4:
+        raise ValueError(f"{name}_codes must be [n_pages, n_kv_heads, page_size, dim*bits/8], got {list(got)}")
+    _on(codes, f"{name}_codes", _I8 if codes.dtype is _I8 else _U8, index, shape)
+    if got[3] != 16 * bits:
+        raise ValueError(f"{name}_codes rows hold {got[3]} bytes, expected 128*bits/8 = {16 * bits}")
+    _on(scales, f"{name}_scales", _F32, index)
+    raise ValueError(f"{name}_scales must be [n_pages, n_kv_heads, page_size, dim/group], got {list(sc)}")
 
 
 def _cuda(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
 def hadq_paged_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -470,29 +499,36 @@ def hadq_paged_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pag
     refused]``; a refused request has total length 0 and slots -1.
     """
     lib = load_library()
-    dev = _cuda(cached_lens, "cached_lens")
+    index = _cuda(cached_lens, "cached_lens")
     batch = cached_lens.numel()
-    _on_device(cached_lens, "cached_lens", torch.int32, dev, (batch,))
-    _on_device(new_lens, "new_lens", torch.int32, dev, (batch,))
-    _on_device(free_pages, "free_pages", torch.int32, dev, (free_pages.numel(),))
+    _on(cached_lens, "cached_lens", _I32, index, (batch,))
+    _on(new_lens, "new_lens", _I32, index, (batch,))
+    _on(free_pages, "free_pages", _I32, index, (free_pages.numel(),))
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, max_pages], got {list(block_table.shape)}")
-    _on_device(block_table, "block_table", torch.int32, dev)
+    _on(block_table, "block_table", _I32, index)
     if slots is None:
         if capacity is None:
             raise ValueError("pass capacity (the rows of slots to fill) or slots")
-        slots = torch.empty(capacity, dtype=torch.int32, device=dev)
+        slots = _new(cached_lens, capacity, _I32, stream)
     else:
-        _on_device(slots, "slots", torch.int32, dev, (slots.numel() if capacity is None else capacity,))
-    outs = []
-    for name, t, n in (("total_lens", total_lens, batch), ("cu_new", cu_new, batch + 1), ("counts", counts, 2)):
-        if t is None:
-            t = torch.empty(n, dtype=torch.int32, device=dev)
-        else:
-            _on_device(t, name, torch.int32, dev, (n,))
-        outs.append(t)
-    total_lens, cu_new, counts = outs
-    _call(lib.hadq_paged_slots, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(), batch, free_pages.data_ptr(),
+        _on(slots, "slots", _I32, index, (slots.numel() if capacity is None else capacity,))
+    new = None
+    if total_lens is None or cu_new is None or counts is None:
+        new = _new(cached_lens, 2 * batch + 3, _I32, stream).split((batch, batch + 1, 2))
+    if total_lens is None:
+        total_lens = new[0]
+    else:
+        _on(total_lens, "total_lens", _I32, index, (batch,))
+    if cu_new is None:
+        cu_new = new[1]
+    else:
+        _on(cu_new, "cu_new", _I32, index, (batch + 1,))
+    if counts is None:
+        counts = new[2]
+    else:
+        _on(counts, "counts", _I32, index, (2,))
+    _call(lib.hadq_paged_slots, index, stream, cached_lens.data_ptr(), new_lens.data_ptr(), batch, free_pages.data_ptr(),
           free_pages.numel(), page_size, block_table.data_ptr(), block_table.shape[1], total_lens.data_ptr(),
           cu_new.data_ptr(), slots.data_ptr(), slots.numel(), counts.data_ptr())
     return slots, total_lens, cu_new, counts
@@ -511,18 +547,18 @@ def hadq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_c
     trailing 1 may be dropped).
     """
     lib = load_library()
-    dev = _cuda(k, "k")
+    index = _cuda(k, "k")
     dim = k.shape[-1] if k.dim() else 0
     G = _resolve(dim, block, group)
-    shape = _pool(k_codes, k_scales, "k", dev, bits, G)
-    _pool(v_codes, v_scales, "v", dev, bits, G, tuple(shape))
-    ks, vs = _rows_view(k, "k", dev, shape[1]), _rows_view(v, "v", dev, shape[1])
+    shape = _pool(k_codes, k_scales, "k", index, bits, G)
+    _pool(v_codes, v_scales, "v", index, bits, G, shape)
+    ks, vs = _rows_view(k, "k", index, shape[1]), _rows_view(v, "v", index, shape[1])
     if v.shape != k.shape:
         raise ValueError("k and v must have the same shape")
-    _on_device(slots, "slots", torch.int32, dev, (k.shape[0],))
+    _on(slots, "slots", _I32, index, (k.shape[0],))
     if signs is not None:
-        _on_device(signs, "signs", torch.int8, dev, (dim,))
-    _call(lib.hadq_paged_append, dev, stream, k.data_ptr(), v.data_ptr(), k.shape[0], ks, vs, shape[1], dim, block, _at(signs),
+        _on(signs, "signs", _I8, index, (dim,))
+    _call(lib.hadq_paged_append, index, stream, k.data_ptr(), v.data_ptr(), k.shape[0], ks, vs, shape[1], dim, block, _at(signs),
           bits, group, slots.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
           shape[0], shape[2])
 
@@ -537,21 +573,21 @@ def hadq_paged_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Te
     outside the pool are left as they were (of a new ``out``: undefined).
     """
     lib = load_library()
-    dev = _cuda(codes, "codes")
-    shape = _pool(codes, scales, "pool", dev, bits, _resolve(128, block, group))
-    _on_device(slots, "slots", torch.int32, dev, (slots.numel(),))
+    index = _cuda(codes, "codes")
+    shape = _pool(codes, scales, "pool", index, bits, _resolve(128, block, group))
+    _on(slots, "slots", _I32, index, (slots.numel(),))
     if signs is not None:
-        _on_device(signs, "signs", torch.int8, dev, (128,))
+        _on(signs, "signs", _I8, index, (128,))
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be bfloat16 or float32")
     want = (slots.numel(), shape[1], 128)
     if out is None:
-        out = torch.empty(want, dtype=out_dtype, device=dev)
+        out = _new(codes, want, out_dtype, stream)
     else:
-        _on_device(out, "out", out_dtype, dev, want)
-    _call(lib.hadq_paged_gather, dev, stream, codes.data_ptr(), scales.data_ptr(), shape[0], shape[2], shape[1], 128, block,
+        _on(out, "out", out_dtype, index, want)
+    _call(lib.hadq_paged_gather, index, stream, codes.data_ptr(), scales.data_ptr(), shape[0], shape[2], shape[1], 128, block,
           _at(signs), bits, group, slots.data_ptr(), slots.numel(), out.data_ptr(),
           HADQ_OUT_F32 if out_dtype == torch.float32 else HADQ_OUT_BF16)
     return out
@@ -584,30 +620,31 @@ def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch
     n_q_heads, 128]``; rows behind the last request are left as they were.
     """
     lib = load_library()
-    dev = _cuda(q, "q")
-    stride = _rows_view(q, "q", dev, None)
+    index = _cuda(q, "q")
+    stride = _rows_view(q, "q", index, None)
     rows, nqh, dim = q.shape
-    shape = _pool(k_codes, k_scales, "k", dev, bits, _resolve(128, block, group))
-    _pool(v_codes, v_scales, "v", dev, bits, _resolve(128, block, group), tuple(shape))
+    G = _resolve(128, block, group)
+    shape = _pool(k_codes, k_scales, "k", index, bits, G)
+    _pool(v_codes, v_scales, "v", index, bits, G, shape)
     batch = total_lens.numel()
-    _on_device(total_lens, "total_lens", torch.int32, dev, (batch,))
-    _on_device(cu_new, "cu_new", torch.int32, dev, (batch + 1,))
+    _on(total_lens, "total_lens", _I32, index, (batch,))
+    _on(cu_new, "cu_new", _I32, index, (batch + 1,))
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, max_pages], got {list(block_table.shape)}")
-    _on_device(block_table, "block_table", torch.int32, dev)
+    _on(block_table, "block_table", _I32, index)
     if signs is not None:
-        _on_device(signs, "signs", torch.int8, dev, (dim,))
+        _on(signs, "signs", _I8, index, (dim,))
     if softmax_scale is None:
         softmax_scale = 1.0 / float(dim) ** 0.5
     if out is None:
-        out = torch.empty((rows, nqh, dim), dtype=torch.bfloat16, device=dev)
+        out = _new(q, (rows, nqh, dim), _BF16, stream)
     else:
-        _on_device(out, "out", torch.bfloat16, dev, (rows, nqh, dim))
+        _on(out, "out", _BF16, index, (rows, nqh, dim))
     if workspace is None:
-        workspace = torch.zeros(hadq_paged_workspace_size(max_new, nqh, shape[1]), dtype=torch.uint8, device=dev)
+        workspace = _new(q, hadq_paged_workspace_size(max_new, nqh, shape[1]), _U8, stream, zero=True)
     else:
-        _on_device(workspace, "workspace", torch.uint8, dev)
-    _call(lib.hadq_paged_attention, dev, stream, q.data_ptr(), rows, stride, cu_new.data_ptr(), total_lens.data_ptr(), batch,
+        _on(workspace, "workspace", _U8, index)
+    _call(lib.hadq_paged_attention, index, stream, q.data_ptr(), rows, stride, cu_new.data_ptr(), total_lens.data_ptr(), batch,
           max_new, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), shape[0], shape[2],
           block_table.data_ptr(), block_table.shape[1], nqh, shape[1], dim, block, _at(signs), bits, group, int(causal),
           window, sinks, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel())

@@ -111,7 +111,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         B.hadq_paged_gather(c, s, i)
     with pytest.raises(ValueError, match="CUDA"):
         B.hadq_paged_attention(q, c, s, c, s, torch.zeros(2, 2, dtype=torch.int32), i, torch.zeros(3, dtype=torch.int32), 1)
-    cpu = torch.device("cpu")
+    cpu = -1  # what get_device() says of CPU tensors
     with pytest.raises(TypeError):
         B._rows_view(q.float(), "q", cpu, None)
     with pytest.raises(ValueError, match="contiguously"):
