@@ -93,6 +93,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -612,52 +619,66 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     }
   } else {
     regs_dec<64>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       // ================================================================ MMAs
+      // The whole warp walks the schedule, so that descriptors and loop
+      // bounds are warp-uniform; one lane issues.
       bool dead = false;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (dead) return;
         if (!mbar_wait(bar, parity, abort)) {
-          tc_give_up(&tl->abort, fault);
+          if (!dead && lane == 0) tc_give_up(&tl->abort, fault);
           dead = true;
         }
+        dead = __any_sync(0xffffffffu, dead);
       };
-      const uint32_t qb = smem_addr(qs), kb = smem_addr(ks), vb = smem_addr(vs);
+      const uint64_t qd = smem_desc(smem_addr(qs), 16, 1024, 2), kd = smem_desc(smem_addr(ks), 16, 1024, 2);
+      const uint64_t vd = smem_desc(smem_addr(vs), kPtHalf, 1024, 2);
       auto mma_s = [&](int m, uint32_t stage) {  // S_m = Q_m K^T
-        if (dead) return;
         tc_fence_after();
+        if (!dead && elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t o = (k >> 2) * kPtHalf + (k & 3) * 32;
-          tc_mma(tmem + uint32_t(128 * m), smem_desc(qb + m * kPtMat + o, 16, 1024, 2), smem_desc(kb + stage * kPtMat + o, 16, 1024, 2),
-                 kPtIdescQK, k > 0);
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
+            tc_mma(tmem + uint32_t(128 * m), qd + uint32_t(m * (kPtMat >> 4) + o), kd + (stage * (kPtMat >> 4) + o), kPtIdescQK, k > 0);
+          }
+          // The softmax reads what the key warps wrote beside the keys
+          // (exponents, cached bits) once S is there: this warp has seen their
+          // arrival and passes it on.  (They cannot wait for k_full
+          // themselves: it may be a phase further on by then.)
+          mbar_arrive(&tl->s_full[m]);
+          tc_commit(&tl->s_full[m]);
         }
-        // The softmax reads what the key warps wrote beside the keys (exponents,
-        // cached bits) once S is there: this thread has seen their arrival and
-        // passes it on.  (They cannot wait for k_full themselves: it may be a
-        // phase further on by then.)
-        mbar_arrive(&tl->s_full[m]);
-        tc_commit(&tl->s_full[m]);
+        __syncwarp();
       };
       auto mma_o = [&](int m, uint32_t stage, bool add) {  // O_m (+)= P_m V
-        if (dead) return;
         tc_fence_after();
+        if (!dead && elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + uint32_t(256 + 128 * m), tmem + uint32_t(128 * m + 8 * k), smem_desc(vb + stage * kPtMat + k * 2048, kPtHalf, 1024, 2),
-                    kPtIdescPV, add || k > 0);
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + uint32_t(256 + 128 * m), tmem + uint32_t(128 * m + 8 * k), vd + (stage * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV,
+                      k > 0 ? 1u : uint32_t(add));
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (!dead && elect_one()) tc_commit(bar);
+        __syncwarp();
       };
       uint32_t n = 0, nu[2] = {0, 0}, np[2] = {0, 0};
       do {
-        const int groups = it.ntok * a.g > 128 ? 2 : 1, tiles = it.i1 - it.i0;
-        for (int m = 0; m < groups; ++m) {
-          wait(&tl->q_full[m], nu[m] & 1);
-          if (m == 0) wait(&tl->k_full[n & 1], (n >> 1) & 1);
-          mma_s(m, n & 1);
+        const int two = __shfl_sync(0xffffffffu, int(it.ntok * a.g > 128), 0), tiles = __shfl_sync(0xffffffffu, it.i1 - it.i0, 0);
+        wait(&tl->q_full[0], nu[0] & 1);
+        wait(&tl->k_full[n & 1], (n >> 1) & 1);
+        mma_s(0, n & 1);
+        if (two) {
+          wait(&tl->q_full[1], nu[1] & 1);
+          mma_s(1, n & 1);
         }
-        if (!dead) tc_commit(&tl->k_empty[n & 1]);
+        commit(&tl->k_empty[n & 1]);
         for (int i = 0; i < tiles; ++i, ++n) {
-          for (int m = 0; m < groups; ++m) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (m == 1 && !two) break;
             wait(&tl->p_full[m], np[m] & 1);
             ++np[m];
             if (m == 0) wait(&tl->v_full[n & 1], (n >> 1) & 1);
@@ -667,18 +688,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
               if (m == 0) wait(&tl->k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
               mma_s(m, (n + 1) & 1);
             } else {
-              if (!dead) tc_commit(&tl->o_full[m]);
+              commit(&tl->o_full[m]);
               ++nu[m];
             }
           }
-          if (!dead) {
-            tc_commit(&tl->v_empty[n & 1]);
-            if (i + 1 < tiles) tc_commit(&tl->k_empty[(n + 1) & 1]);
-          }
+          commit(&tl->v_empty[n & 1]);
+          if (i + 1 < tiles) commit(&tl->k_empty[(n + 1) & 1]);
         }
       } while (it.next(a, per));
       // every MMA is complete before TMEM is freed (passes at once normally)
-      if (!dead && n > 0) (void)mbar_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
+      if (!dead) (void)mbar_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
     }
   }
 
