@@ -17,15 +17,23 @@
 //    2^-e of it.  The reference rises only by more than 2^8, so that O, in
 //    TMEM, is rarely rescaled.  m, l and O are float32.
 //
-// Roles (one CTA per SM, 512 threads, registers dealt by setmaxnreg):
-//  * warps 0-3 and 4-7: softmax of group 0 and 1, a row per thread.  They also
-//    rotate the next unit's queries into shared memory (H_128 in registers)
-//    before they finish a unit (rotate back, normalise, store);
-//  * warps 8-11: a key per thread: load codes one tile ahead into registers,
-//    convert, scale and store them in the swizzled layout both products read
-//    (K: K-major, V: MN-major; the same bytes);
-//  * warp 12: one thread issues the MMAs.  Group 0's softmax runs under group
-//    1's MMAs and the other way round.
+// Roles (one CTA per SM, five warpgroups, registers dealt by setmaxnreg):
+//  * warps 0-3 and 4-7: softmax of group 0 and 1, a row per thread.  A row is
+//    read from TMEM in two halves: both for the maximum, then the second one's
+//    weights from registers and the first one's from a second read, so that a
+//    thread never holds more than half a row.  P takes the columns of S's
+//    second half.  They also rotate the next unit's queries into shared memory
+//    (H_128 in registers) before they finish a unit (rotate back, normalise,
+//    store);
+//  * warps 8-11 (keys) and 12-15 (values): a cached row per thread: load codes
+//    one tile ahead into registers, convert, scale and store them in the
+//    swizzled layout both products read (K: K-major, V: MN-major; the same
+//    bytes, and the same code);
+//  * warp 16 issues the MMAs.  Group 0's softmax runs under group 1's MMAs and
+//    the other way round.
+// The roles' loops are kept short (loops over quarters of a row instead of
+// straight code): with four instruction streams on an SM, fetching them cost
+// more than the work did (7400 cycles a tile with everything unrolled).
 // The columns of Q, K, V are stored in the order in which one mask finds
 // them, dim 8 c + (0, 4, 1, 5, 2, 6, 3, 7): scores do not change, and H_128 of
 // O is the same up to that order.
@@ -49,7 +57,7 @@
 
 namespace hadq {
 
-constexpr int kPtThreads = 512;
+constexpr int kPtThreads = 640;
 constexpr int kPtRows = 256;  // query rows per unit
 constexpr int kPtTile = 128;  // keys per tile
 constexpr int kPtHalf = 128 * 128;            // bytes of 64 columns x 128 rows
@@ -61,71 +69,8 @@ constexpr int kPtCounterBase = 1024;          // first of this kernel's arrival 
 constexpr uint32_t kPtIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kPtIdescPV = kPtIdescQK | (1u << 16);  // B MN-major
 
-struct PtTail {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  int kexp[4], vexp[4];     // exponents of the last four tiles' scales
-  uint32_t ok[4][4];        // keys of the tile that are cached (bit per key)
-  uint32_t red[2][4];       // group maxima of |q|
-  uint32_t dred[2][2][4];   // tile maxima of the scales: [parity][K, V][warp]
-  uint32_t sgn[4];          // sign bits of the 128 columns
-  int last[2];
-  uint32_t tmem_base;
-  uint32_t abort;
-  PagedPlanSmem plan;
-};
-static_assert(offsetof(PtTail, ok) % 16 == 0, "the cached bits are read as 16-byte vectors");
-__host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + size_t(6) * kPtMat + sizeof(PtTail); }
-
-// D[tmem] (+)= A[tmem] B over K = 16.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-__device__ __forceinline__ void fma2(float& a, float& b, float m, float c) {
-  uint64_t X, M, C, R;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(M) : "f"(m));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(C) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(R) : "l"(X), "l"(M), "l"(C));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(R));
-}
-__device__ __forceinline__ void sum2(float& a, float& b, float x, float y) {
-  uint64_t A, X, R;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(A) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(x), "f"(y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(A), "l"(X));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(R));
-}
-// 2^e for any integer e (0 and the largest power of two outside the range).
-__device__ __forceinline__ float pow2_clamped(int e) {
-  return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);
-}
-
-// A CTA's units and tiles in order; every role walks its own copy.
+// A CTA's units and tiles in order.  Every warp walks its own copy, in shared
+// memory: in registers it would be spilled in the loops that matter.
 struct PtIter {
   int64_t at, end;     // next tile on the line, end of the CTA's piece
   int64_t ustart;      // first tile of the unit on the line
@@ -163,7 +108,142 @@ struct PtIter {
     cut(0);
     return true;
   }
+  // next() by one lane for the whole warp.
+  __device__ __forceinline__ bool warp_next(const PagedAttnArgs& a, int per) {
+    int ok = 0;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ok = next(a, per);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  }
 };
+
+struct PtTail {
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  int kexp[4], vexp[4];     // exponents of the last four tiles' scales
+  uint32_t ok[4][4];        // keys of the tile that are cached (bit per key)
+  uint32_t red[2][4];       // group maxima of |q|
+  uint32_t dred[2][2][2][4];  // tile maxima of the scales: [role][parity][K, V][warp]
+  uint32_t sgn[4];          // sign bits of the 128 columns
+  int last[2];
+  uint32_t tmem_base;
+  uint32_t abort;
+  PagedPlanSmem plan;
+  PtIter it[17], next[8];  // by warp; the softmax warps also look one unit ahead
+};
+static_assert(offsetof(PtTail, ok) % 16 == 0, "the cached bits are read as 16-byte vectors");
+__host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + size_t(6) * kPtMat + sizeof(PtTail); }
+
+// Wait for the phase of `parity`; false after kTcWaitNs, or as soon as another
+// role has given up.  The clock and the abort word are read once in 64 tries:
+// a read of the clock costs more than the waits that matter.
+__device__ __forceinline__ bool pt_wait(uint64_t* b, uint32_t parity, const volatile uint32_t* abort) {
+  unsigned long long t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    if (mbar_test(b, parity)) return true;
+    if ((spin & 63) == 0) {
+      if (abort && *abort) return false;
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kTcWaitNs) return false;
+    }
+  }
+}
+
+// The upper word of every operand's descriptor: stride 1024 bytes between
+// groups of eight rows, version, 128-byte swizzle; the lower words (address,
+// leading stride) are all a step has to change.
+constexpr uint32_t kPtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t pt_desc_lo(const void* p, uint32_t lbo) { return ((smem_addr(p) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+
+// D[tmem] (+)= A B over K = 16, A from shared memory or (ts) from TMEM.
+__device__ __forceinline__ void pt_mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi)
+      : "memory");
+}
+#define HADQ_R32 \
+  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, " \
+  "%24, %25, %26, %27, %28, %29, %30, %31"
+#define HADQ_R64 \
+  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, " \
+  "%24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, " \
+  "%46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+// 32 lanes x 32 or 64 columns of TMEM; the wait is part of the statement.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" HADQ_R64 "}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
+        "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+        "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {" HADQ_R32 "};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+               "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+               "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+               "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Registers of a thread: 640 threads launch with 96 each, 480 for the five
+// warps of a scheduler; two softmax warps, a key, a value and the MMA warp
+// get 2 * 144 + 2 * 72 + 48.
+constexpr int kPtRegsSoftmax = 144, kPtRegsCodes = 72, kPtRegsMma = 48;
+static_assert(2 * kPtRegsSoftmax + 2 * kPtRegsCodes + kPtRegsMma <= 5 * 96, "the launch's registers");
+
+template <uint32_t V>
+struct PtInt {
+  static constexpr uint32_t value = V;
+};
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void fma2(float& a, float& b, float m, float c) {
+  uint64_t X, M, C, R;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(M) : "f"(m));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(C) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(R) : "l"(X), "l"(M), "l"(C));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(R));
+}
+__device__ __forceinline__ void sum2(float& a, float& b, float x, float y) {
+  uint64_t A, X, R;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(A) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(X) : "f"(x), "f"(y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(A), "l"(X));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(R));
+}
+// 2^e for any integer e (0 and the largest power of two outside the range).
+__device__ __forceinline__ float pow2_clamped(int e) {
+  return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);
+}
 
 template <int NG, int BITS>
 __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedAttnArgs a, unsigned* fault) {
@@ -205,47 +285,51 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     const uint32_t bits = __ballot_sync(0xffffffffu, a.signs && a.signs[tid] < 0);
     if (lane == 0) tl->sgn[warp] = bits;
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tl->tmem_base)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tl->tmem_base;  // S0, S1, O0, O1: 128 columns each
+  // All 512 columns are this CTA's, so they start at column 0: S0, S1, O0, O1
+  // of 128 columns each, at constant addresses.
+  constexpr uint32_t tmem = 0;
 
-  PtIter it;
-  it.at = pc.at;
-  it.end = pc.end;
-  it.b = pc.b;
-  it.rq = paged_req(a, pc.b);
-  {
-    const int64_t ph = head_tiles(it.rq);
-    it.h = int(pc.in_request / ph);
-    int64_t u = pc.in_request - it.h * ph;
-    it.qt = 0;
+  if (warp < 17 && lane == 0) {
+    PtIter f;
+    f.at = pc.at;
+    f.end = pc.end;
+    f.b = pc.b;
+    f.rq = paged_req(a, pc.b);
+    const int64_t ph = head_tiles(f.rq);
+    f.h = int(pc.in_request / ph);
+    int64_t u = pc.in_request - f.h * ph;
+    f.qt = 0;
     for (;;) {
-      it.fill(a, per);
-      if (u < it.tl.count) break;
-      u -= it.tl.count;
-      ++it.qt;
+      f.fill(a, per);
+      if (u < f.tl.count) break;
+      u -= f.tl.count;
+      ++f.qt;
     }
-    it.cut(u);
+    f.cut(u);
+    tl->it[warp] = f;
+    if (warp < 8) tl->next[warp] = f;
   }
+  __syncwarp();
 
   if (warp < 8) {
     // =============================================== softmax, queries, output
-    regs_inc<176>();
+    regs_inc<kPtRegsSoftmax>();
     const int m = warp >> 2, r = tid & 127;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + uint32_t(128 * m), tO = tmem + lanes + uint32_t(256 + 128 * m);
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!mbar_wait(bar, parity, abort)) {
+      if (!pt_wait(bar, parity, abort)) {
         if (!dead) tc_give_up(&tl->abort, fault);
         dead = true;
       }
-      dead = __any_sync(0xffffffffu, dead);
     };
     int eq = 0;  // the group's queries are scaled by 2^eq
 
@@ -300,107 +384,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       if (lane == 0) mbar_arrive(&tl->q_full[m]);
     };
 
-    if (128 * m < it.ntok * a.g) load_queries(it);
     uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
-    for (bool more = true; more;) {
-      const bool active = 128 * m < it.ntok * a.g;
-      float M = -INFINITY, l = 0.f;
-      if (active) {
-        const int off = it.rq.len - it.rq.n;
-        const int row = min(128 * m + r, it.ntok * a.g - 1), tok = it.first + row / a.g;
-        const int lim = a.causal ? min(it.rq.len, off + tok + 1) : it.rq.len;
-        const int low = a.window > 0 ? off + tok - a.window + 1 : 0;
-        // keys that every row of the group sees: below all_lim, from all_low on
-        const int f_tok = it.first + 128 * m / a.g, l_tok = it.first + min(128 * m + 127, it.ntok * a.g - 1) / a.g;
-        const int all_lim = a.causal ? off + f_tok + 1 : it.rq.len;
-        const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
-        for (int i = it.i0; i < it.i1; ++i, ++n, ++ns) {
-          wait(&tl->s_full[m], ns & 1);
-          tc_fence_after();
-          const int ve = tl->vexp[n & 3];
-          const float f = pow2_clamped(tl->kexp[n & 3] - 134 - eq), vexp = float(ve - 127);
-          const uint4 ok = *reinterpret_cast<const uint4*>(tl->ok[n & 3]);
-          float s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
-          const int t0 = it.key0(i);
-          const bool full = (ok.x & ok.y & ok.z & ok.w) == 0xffffffffu;
-          if (!full || t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low)) {
-            const uint32_t okw[4] = {ok.x, ok.y, ok.z, ok.w};
-            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int tc = t0 + 32 * c;
-              uint32_t see = okw[c] & below(lim - tc);
-              if (a.window > 0) see &= ~below(low - tc) | below(a.sinks - tc);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((see >> k) & 1u)) s[32 * c + k] = -INFINITY;
-            }
-          }
-          float top0 = s[0], top1 = s[1], top2 = s[2], top3 = s[3];
-#pragma unroll
-          for (int k = 4; k < 124; k += 8) {
-            top0 = max3(top0, s[k], s[k + 1]);
-            top1 = max3(top1, s[k + 2], s[k + 3]);
-            top2 = max3(top2, s[k + 4], s[k + 5]);
-            top3 = max3(top3, s[k + 6], s[k + 7]);
-          }
-          top0 = max3(top0, s[124], s[125]);
-          top1 = max3(top1, s[126], s[127]);
-          const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), f, vexp);
-          const bool need = top > M + kAttnSlack;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2f(M - top) : 1.f;
-            if (need) M = top;
-            l *= alpha;
-            if (i > it.i0) {  // the previous tiles' products are complete: S came after them
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-                    "tcgen05.wait::ld.sync.aligned;"
-                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
-                      "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                    : "r"(tO + 16 * c)
-                    : "memory");
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st16(tO + 16 * c, o);
-              }
-            }
-          }
-          const float sub = M == -INFINITY ? 0.f : vexp - M;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x = s[32 * c + 2 * k], y = s[32 * c + 2 * k + 1];
-              fma2(x, y, f, sub);
-              x = exp2_ftz(x);
-              y = exp2_ftz(y);
-              if (k & 1) sum2(l2, l3, x, y); else sum2(l0, l1, x, y);
-              p[k] = cvt_f16x2(x, y);
-            }
-            tmem_st16(tS + 16 * c, p);
-          }
-          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(127 - ve), l);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tl->p_full[m]);
-        }
-      } else {
-        n += it.i1 - it.i0;
-      }
-
-      // ---- next unit's queries, then this unit's output ----
-      PtIter nx = it;
-      more = nx.next(a, per);
-      if (more && 128 * m < nx.ntok * a.g) load_queries(nx);
+    bool active = false;             // the group has rows in unit `it`
+    float M = -INFINITY, l = 0.f;
+    PtIter &it = tl->it[warp], &nx = tl->next[warp];
+    for (bool more = true;;) {
+      // ---- the next unit's queries, then the output of the unit just done ----
+      const bool next_active = more && 128 * m < nx.ntok * a.g;
+      if (next_active) load_queries(nx);
       if (active) {
         wait(&tl->o_full[m], nu & 1);
         ++nu;
@@ -474,236 +465,329 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           }
         }
       }
-      it = nx;
+      if (!more) break;
+      __syncwarp();
+      if (lane == 0) it = nx;
+      __syncwarp();
+      active = next_active;
+      M = -INFINITY;
+      l = 0.f;
+      if (active) {
+        const int off = it.rq.len - it.rq.n;
+        const int row = min(128 * m + r, it.ntok * a.g - 1), tok = it.first + row / a.g;
+        const int lim = a.causal ? min(it.rq.len, off + tok + 1) : it.rq.len;
+        const int low = a.window > 0 ? off + tok - a.window + 1 : 0;
+        // keys that every row of the group sees: below all_lim, from all_low on
+        const int f_tok = it.first + 128 * m / a.g, l_tok = it.first + min(128 * m + 127, it.ntok * a.g - 1) / a.g;
+        const int all_lim = a.causal ? off + f_tok + 1 : it.rq.len;
+        const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
+        for (int i = it.i0; i < it.i1; ++i, ++n, ++ns) {
+          wait(&tl->s_full[m], ns & 1);
+          tc_fence_after();
+          const int ve = tl->vexp[n & 3];
+          const float f = pow2_clamped(tl->kexp[n & 3] - 134 - eq), vexp = float(ve - 127);
+          const uint4 ok = *reinterpret_cast<const uint4*>(tl->ok[n & 3]);
+          const int t0 = it.key0(i);
+          const bool full = (ok.x & ok.y & ok.z & ok.w) == 0xffffffffu;
+          if (!full || t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low)) {  // put -inf where a row sees nothing
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int tc = t0 + 32 * c;
+              auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
+              uint32_t see = tl->ok[n & 3][c] & below(lim - tc);
+              if (a.window > 0) see &= ~below(low - tc) | below(a.sinks - tc);
+              float x[32];
+              tmem_ld32(tS + 32 * c, x);
+              uint32_t y[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = (see >> k) & 1u ? __float_as_uint(x[k]) : 0xff800000u;
+              tmem_st32(tS + 32 * c, y);
+            }
+            tmem_wait_st();
+          }
+          uint32_t s[64];
+          float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld64(tS + 64 * c, s);
+#pragma unroll
+            for (int k = 0; k < 64; k += 8) {
+              top0 = max3(top0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+              top1 = max3(top1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+              top2 = max3(top2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+              top3 = max3(top3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+            }
+          }
+          const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), f, vexp);
+          const bool need = top > M + kAttnSlack;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? exp2f(M - top) : 1.f;
+            if (need) M = top;
+            l *= alpha;
+            if (i > it.i0) {  // the previous tiles' products are complete: S came after them
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float o[32];
+                tmem_ld32(tO + 32 * c, o);
+                uint32_t y[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(o[k] * alpha);
+                tmem_st32(tO + 32 * c, y);
+              }
+            }
+          }
+          const float sub = M == -INFINITY ? 0.f : vexp - M;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll 1
+          for (int c = 1; c >= 0; --c) {  // the second half is in registers
+            if (c == 0) tmem_ld64(tS, s);
+            uint32_t p[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float x = __uint_as_float(s[2 * k]), y = __uint_as_float(s[2 * k + 1]);
+              fma2(x, y, f, sub);
+              x = exp2_ftz(x);
+              y = exp2_ftz(y);
+              if (k & 1) sum2(l2, l3, x, y); else sum2(l0, l1, x, y);
+              p[k] = cvt_f16x2(x, y);
+            }
+            tmem_st32(tS + 64 + 32 * c, p);
+          }
+          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(127 - ve), l);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tl->p_full[m]);
+        }
+      } else {
+        n += it.i1 - it.i0;
+      }
+      more = nx.warp_next(a, per);
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ======================================================= keys and values
-    regs_dec<96>();
+    regs_dec<kPtRegsCodes>();
+    const int role = (warp - 8) >> 2;  // 0: keys, 1: values
     const int t = tid & 127, w = warp & 3;
     constexpr int RB = 16 * BITS, NV = RB / 16;  // 16-byte pieces per row
+    const uint8_t* codes = role ? a.v_codes : a.k_codes;
+    uint64_t* full = role ? tl->v_full : tl->k_full;
+    uint64_t* empty = role ? tl->v_empty : tl->k_empty;
+    uint8_t* mat = (role ? vs : ks) + t * 128;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!mbar_wait(bar, parity, abort)) {
+      if (!pt_wait(bar, parity, abort)) {
         if (!dead) tc_give_up(&tl->abort, fault);
         dead = true;
       }
-      dead = __any_sync(0xffffffffu, dead);
     };
     // The iterator runs ahead of the tile in work: page ids by two tiles,
-    // codes by one.
+    // codes and scales by one.
+    PtIter& it = tl->it[warp];
     int i = it.i0;
     bool more = true;
-    int64_t src = -1;  // row in the pool of this thread's key of the tile to load next, -1: none
+    int page = -1, where = 0;  // of the tile to load next: this row's page, head and offset in it
+    int hd = 0;
     auto find = [&]() {
-      src = -1;
+      page = -1;
       if (!more) return;
       const int pos = it.key0(i) + t;
-      if (pos < it.tl.kv_end) {
-        const int p = __ldg(a.table + int64_t(it.b) * a.max_pages + (pos >> a.page_log2));
-        if (unsigned(p) < unsigned(a.n_pages))
-          src = ((int64_t(p) * a.nkv + it.h) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
-      }
+      hd = it.h;
+      where = pos & ((1 << a.page_log2) - 1);
+      if (pos < it.tl.kv_end) page = __ldg(a.table + int64_t(it.b) * a.max_pages + (pos >> a.page_log2));
       if (++i == it.i1) {
-        more = it.next(a, per);
+        more = it.warp_next(a, per);
         i = it.i0;
       }
     };
-    uint4 kr[NV], vr[NV];
+    uint4 cur[NV];
     float kscl[NG], vscl[NG];
-    bool have = false;  // the loaded key is cached
-    int64_t vsrc = -1;
-    auto load_k = [&]() {
-      have = src >= 0;
-      vsrc = src;
-#pragma unroll
-      for (int x = 0; x < NV; ++x) kr[x] = have ? __ldg(reinterpret_cast<const uint4*>(a.k_codes + src * RB) + x) : make_uint4(0u, 0u, 0u, 0u);
+    bool have = false;           // the next row to load is cached
+    const uint4* src = nullptr;  // its codes
+    auto locate = [&]() {        // the found row: its scales now, its codes piece by piece
+      have = unsigned(page) < unsigned(a.n_pages);
+      const int64_t row = have ? ((int64_t(page) * a.nkv + hd) << a.page_log2) + where : 0;
+      src = reinterpret_cast<const uint4*>(codes + row * RB);
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
-        kscl[q] = have ? __ldg(a.k_scales + src * NG + q) : 0.f;
-        vscl[q] = have ? __ldg(a.v_scales + src * NG + q) : 0.f;
+        kscl[q] = have ? __ldg(a.k_scales + row * NG + q) : 0.f;
+        vscl[q] = have ? __ldg(a.v_scales + row * NG + q) : 0.f;
       }
     };
-    auto load_v = [&]() {
+    auto piece = [&](int x) { return have ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u); };
+    find();
+    locate();
 #pragma unroll
-      for (int x = 0; x < NV; ++x) vr[x] = vsrc >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.v_codes + vsrc * RB) + x) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    // codes -> f16 pairs (e, e + 4) of 8 columns
-    auto pairs = [&](const uint4 (&raw)[NV], int c, uint32_t (&p)[4]) {
-      if constexpr (BITS == 4) {
-        const uint4 x = raw[c >> 2];
-        const uint32_t word = (c & 3) == 0 ? x.x : (c & 3) == 1 ? x.y : (c & 3) == 2 ? x.z : x.w;
-        i4x4_to_f16_tokens(word, p);
-      } else {
-        const uint4 x = raw[c >> 1];
-        i8x8_to_f16_pairs((c & 1) ? x.z : x.x, (c & 1) ? x.w : x.y, p);
-      }
-    };
+    for (int x = 0; x < NV; ++x) cur[x] = piece(x);
     find();
-    load_k();
-    load_v();
-    find();
+    const uint32_t offs[4] = {uint32_t((0 ^ (t & 7)) << 4), uint32_t((1 ^ (t & 7)) << 4), uint32_t((2 ^ (t & 7)) << 4), uint32_t((3 ^ (t & 7)) << 4)};
     const uint32_t total = uint32_t(pc.end - pc.at);
+#pragma unroll 1
     for (uint32_t n = 0; n < total; ++n) {
       const int s = n & 1;
       const uint32_t ph = (n >> 1) & 1;
       // exponents of the tile's largest scales
-      float kt = 0.f, vt = 0.f;
+      float kt = 0.f, vt = 0.f, own[NG];
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
-        kscl[q] = clean_scale(kscl[q]);
-        vscl[q] = clean_scale(vscl[q]);
-        kt = fmaxf(kt, kscl[q]);
-        vt = fmaxf(vt, vscl[q]);
+        const float x = clean_scale(kscl[q]), y = clean_scale(vscl[q]);
+        kt = fmaxf(kt, x);
+        vt = fmaxf(vt, y);
+        own[q] = role ? y : x;
       }
       const uint32_t kw = __reduce_max_sync(0xffffffffu, __float_as_uint(kt)), vw = __reduce_max_sync(0xffffffffu, __float_as_uint(vt));
       const uint32_t okw = __ballot_sync(0xffffffffu, have);
       if (lane == 0) {
-        tl->dred[s][0][w] = kw;
-        tl->dred[s][1][w] = vw;
+        tl->dred[role][s][0][w] = kw;
+        tl->dred[role][s][1][w] = vw;
       }
-      wait(&tl->k_empty[s], ph ^ 1u);
-      if (lane == 0) tl->ok[n & 3][w] = okw;
-      named_bar_sync(3, 128);
-      const uint32_t (&dk)[4] = tl->dred[s][0], (&dv)[4] = tl->dred[s][1];
+      locate();  // the next tile's rows
+      find();
+      wait(&empty[s], ph ^ 1u);
+      if (role == 0 && lane == 0) tl->ok[n & 3][w] = okw;
+      named_bar_sync(3 + role, 128);
+      const uint32_t (&dk)[4] = tl->dred[role][s][0], (&dv)[4] = tl->dred[role][s][1];
       const int ke = min(max(int(max(max(dk[0], dk[1]), max(dk[2], dk[3])) >> 23), 27), 227);
       const int ve = min(max(int(max(max(dv[0], dv[1]), max(dv[2], dv[3])) >> 23), 27), 227);
-      if (t == 0) {
+      if (role == 0 && t == 0) {
         tl->kexp[n & 3] = ke;
         tl->vexp[n & 3] = ve;
       }
-      const float kup = pow2_clamped(134 - ke), vup = pow2_clamped(134 - ve);  // largest scale to [2^7, 2^8)
-      uint32_t khi[NG], klo[NG], vhi[NG];
+      const float up = pow2_clamped(134 - (role ? ve : ke));  // largest scale to [2^7, 2^8)
+      uint32_t hi[NG], lo[NG];
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
-        const float x = kscl[q] * kup;
-        khi[q] = cvt_f16x2(x, x);
-        float hi;
-        asm("{.reg .f16 l, h;\n mov.b32 {l, h}, %1;\n cvt.f32.f16 %0, l;}" : "=f"(hi) : "r"(khi[q]));
-        klo[q] = cvt_f16x2(x - hi, x - hi);
-        const float y = vscl[q] * vup;
-        vhi[q] = cvt_f16x2(y, y);
+        const float x = own[q] * up;
+        hi[q] = cvt_f16x2(x, x);
+        float h;
+        asm("{.reg .f16 l, h;\n mov.b32 {l, h}, %1;\n cvt.f32.f16 %0, l;}" : "=f"(h) : "r"(hi[q]));
+        lo[q] = cvt_f16x2(x - h, x - h);
       }
-      uint8_t* kd = ks + s * kPtMat + t * 128;
+      uint8_t* dst = mat + s * kPtMat;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 16; ++c) {  // eight columns; a used-up piece is refilled with the next tile's
+        constexpr int CP = 16 / NV;   // chunks per piece
+        const uint4 v = cur[c / CP];
         uint32_t p[4];
-        pairs(kr, c, p);
+        if constexpr (BITS == 4)
+          i4x4_to_f16_tokens((c & 3) == 0 ? v.x : (c & 3) == 1 ? v.y : (c & 3) == 2 ? v.z : v.w, p);
+        else
+          i8x8_to_f16_pairs((c & 1) ? v.z : v.x, (c & 1) ? v.w : v.y, p);
         const int q = c * NG / 16;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t y = f16x2_mul(p[x], klo[q]);
-          asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[x]) : "r"(p[x]), "r"(khi[q]), "r"(y));
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t z = f16x2_mul(p[y], lo[q]);
+          asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[y]) : "r"(p[y]), "r"(hi[q]), "r"(z));
         }
-        *reinterpret_cast<uint4*>(kd + (c >> 3) * kPtHalf + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (offs[c & 3] ^ ((c & 4) << 4))) = make_uint4(p[0], p[1], p[2], p[3]);
+        if (c % CP == CP - 1) cur[c / CP] = piece(c / CP);
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tl->k_full[s]);
-      load_k();  // the next tile's (vr still holds this one's values)
-      find();
-      wait(&tl->v_empty[s], ph ^ 1u);
-      uint8_t* vd = vs + s * kPtMat + t * 128;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        uint32_t p[4];
-        pairs(vr, c, p);
-        const int q = c * NG / 16;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) p[x] = f16x2_mul(p[x], vhi[q]);
-        *reinterpret_cast<uint4*>(vd + (c >> 3) * kPtHalf + (((c & 7) ^ (t & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tl->v_full[s]);
-      load_v();
+      if (lane == 0) mbar_arrive(&full[s]);
     }
   } else {
-    regs_dec<64>();
-    if (warp == 12) {
-      // ================================================================ MMAs
-      // The whole warp walks the schedule, so that descriptors and loop
-      // bounds are warp-uniform; one lane issues.
-      bool dead = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!mbar_wait(bar, parity, abort)) {
-          if (!dead && lane == 0) tc_give_up(&tl->abort, fault);
-          dead = true;
-        }
-        dead = __any_sync(0xffffffffu, dead);
-      };
-      const uint64_t qd = smem_desc(smem_addr(qs), 16, 1024, 2), kd = smem_desc(smem_addr(ks), 16, 1024, 2);
-      const uint64_t vd = smem_desc(smem_addr(vs), kPtHalf, 1024, 2);
-      auto mma_s = [&](int m, uint32_t stage) {  // S_m = Q_m K^T
-        tc_fence_after();
-        if (!dead && elect_one()) {
+    regs_dec<kPtRegsMma>();
+    if (warp == 16) {
+    // ================================================================== MMAs
+    // The whole warp walks the schedule, one lane issues.  Descriptors and
+    // TMEM addresses are sums of warp-uniform bases and constants (group and
+    // stage unrolled), so that an issue costs no moves to uniform registers.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!pt_wait(bar, parity, abort)) {
+        if (!dead && lane == 0) tc_give_up(&tl->abort, fault);
+        dead = true;
+      }
+    };
+    const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtHalf);
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one() && !dead) tc_commit(bar);
+      __syncwarp();
+    };
+    auto mma_s = [&](auto M, auto STAGE) {  // S_m = Q_m K^T
+      constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
+      tc_fence_after();
+      if (elect_one() && !dead) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
-            tc_mma(tmem + uint32_t(128 * m), qd + uint32_t(m * (kPtMat >> 4) + o), kd + (stage * (kPtMat >> 4) + o), kPtIdescQK, k > 0);
-          }
-          // The softmax reads what the key warps wrote beside the keys
-          // (exponents, cached bits) once S is there: this warp has seen their
-          // arrival and passes it on.  (They cannot wait for k_full
-          // themselves: it may be a phase further on by then.)
-          mbar_arrive(&tl->s_full[m]);
-          tc_commit(&tl->s_full[m]);
+        for (uint32_t k = 0; k < 8; ++k) {
+          const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
+          pt_mma_ss(128 * m, qd + (m * (kPtMat >> 4) + o), kd + (st * (kPtMat >> 4) + o), kPtIdescQK, k > 0);
         }
-        __syncwarp();
-      };
-      auto mma_o = [&](int m, uint32_t stage, bool add) {  // O_m (+)= P_m V
-        tc_fence_after();
-        if (!dead && elect_one()) {
+        // The softmax reads what the key warps wrote beside the keys
+        // (exponents, cached bits) once S is there: this warp has seen their
+        // arrival and passes it on.  (They cannot wait for k_full themselves:
+        // it may be a phase further on by then.)
+        mbar_arrive(&tl->s_full[m]);
+        tc_commit(&tl->s_full[m]);
+      }
+      __syncwarp();
+    };
+    auto mma_o = [&](auto M, auto STAGE, bool add) {  // O_m (+)= P_m V
+      constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
+      tc_fence_after();
+      if (elect_one() && !dead) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + uint32_t(256 + 128 * m), tmem + uint32_t(128 * m + 8 * k), vd + (stage * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV,
-                      k > 0 ? 1u : uint32_t(add));
+        for (uint32_t k = 0; k < 8; ++k)
+          pt_mma_ts(256 + 128 * m, 128 * m + 64 + 8 * k, vd + (st * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV, k > 0 ? 1u : uint32_t(add));
+      }
+      __syncwarp();
+    };
+    constexpr PtInt<0> c0{};
+    constexpr PtInt<1> c1{};
+    PtIter& it = tl->it[16];
+    uint32_t n = 0, pu0 = 0, pu1 = 0, pp0 = 0, pp1 = 0;  // parities of the groups' units and tiles
+    do {
+      const bool two = __shfl_sync(0xffffffffu, int(it.ntok * a.g > 128), 0);
+      const int tiles = __shfl_sync(0xffffffffu, it.i1 - it.i0, 0);
+      wait(&tl->q_full[0], pu0);
+      wait(&tl->k_full[n & 1], (n >> 1) & 1);
+      if (n & 1) mma_s(c0, c1); else mma_s(c0, c0);
+      if (two) {
+        wait(&tl->q_full[1], pu1);
+        if (n & 1) mma_s(c1, c1); else mma_s(c1, c0);
+      }
+      commit(&tl->k_empty[n & 1]);
+      // Tile i: O += P V, then S of tile i + 1, for either group.
+      auto tile = [&](auto STAGE, auto OTHER, int i) {
+        constexpr uint32_t st = decltype(STAGE)::value, ot = decltype(OTHER)::value;
+        const bool next = i + 1 < tiles;
+        wait(&tl->p_full[0], pp0);
+        pp0 ^= 1;
+        wait(&tl->v_full[st], (n >> 1) & 1);
+        if (i == 0) wait(&tl->o_empty[0], pu0 ^ 1u);
+        mma_o(c0, STAGE, i > 0);
+        if (next) {
+          wait(&tl->k_full[ot], ((n + 1) >> 1) & 1);
+          mma_s(c0, OTHER);
+        } else {
+          commit(&tl->o_full[0]);
         }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (!dead && elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      uint32_t n = 0, nu[2] = {0, 0}, np[2] = {0, 0};
-      do {
-        const int two = __shfl_sync(0xffffffffu, int(it.ntok * a.g > 128), 0), tiles = __shfl_sync(0xffffffffu, it.i1 - it.i0, 0);
-        wait(&tl->q_full[0], nu[0] & 1);
-        wait(&tl->k_full[n & 1], (n >> 1) & 1);
-        mma_s(0, n & 1);
         if (two) {
-          wait(&tl->q_full[1], nu[1] & 1);
-          mma_s(1, n & 1);
+          wait(&tl->p_full[1], pp1);
+          pp1 ^= 1;
+          if (i == 0) wait(&tl->o_empty[1], pu1 ^ 1u);
+          mma_o(c1, STAGE, i > 0);
+          if (next) mma_s(c1, OTHER); else commit(&tl->o_full[1]);
         }
-        commit(&tl->k_empty[n & 1]);
-        for (int i = 0; i < tiles; ++i, ++n) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (m == 1 && !two) break;
-            wait(&tl->p_full[m], np[m] & 1);
-            ++np[m];
-            if (m == 0) wait(&tl->v_full[n & 1], (n >> 1) & 1);
-            if (i == 0) wait(&tl->o_empty[m], (nu[m] & 1) ^ 1u);
-            mma_o(m, n & 1, i > 0);
-            if (i + 1 < tiles) {
-              if (m == 0) wait(&tl->k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-              mma_s(m, (n + 1) & 1);
-            } else {
-              commit(&tl->o_full[m]);
-              ++nu[m];
-            }
-          }
-          commit(&tl->v_empty[n & 1]);
-          if (i + 1 < tiles) commit(&tl->k_empty[(n + 1) & 1]);
-        }
-      } while (it.next(a, per));
-      // every MMA is complete before TMEM is freed (passes at once normally)
-      if (!dead) (void)mbar_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
+        commit(&tl->v_empty[st]);
+        if (next) commit(&tl->k_empty[ot]);
+      };
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i, ++n) {
+        if (n & 1) tile(c1, c0, i); else tile(c0, c1, i);
+      }
+      pu0 ^= 1;
+      if (two) pu1 ^= 1;
+    } while (it.warp_next(a, per));
+    // every MMA is complete before TMEM is freed (passes at once normally)
+    if (!dead) (void)pt_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
