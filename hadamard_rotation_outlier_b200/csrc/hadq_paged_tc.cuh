@@ -135,18 +135,19 @@ struct PtTail {
 static_assert(offsetof(PtTail, ok) % 16 == 0, "the cached bits are read as 16-byte vectors");
 __host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + size_t(6) * kPtMat + sizeof(PtTail); }
 
-// Wait for the phase of `parity`; false after kTcWaitNs, or as soon as another
-// role has given up.  The clock and the abort word are read once in 64 tries:
-// a read of the clock costs more than the waits that matter.
+// Wait for the phase of `parity`; false after about a second, or as soon as
+// another role has given up.  The clock (the SM's own, which is read at once)
+// and the abort word are looked at once in 64 tries.
+constexpr long long kPtWaitCycles = 2000000000ll;
 __device__ __forceinline__ bool pt_wait(uint64_t* b, uint32_t parity, const volatile uint32_t* abort) {
-  unsigned long long t0 = 0;
+  long long t0 = 0;
   for (uint32_t spin = 1;; ++spin) {
     if (mbar_test(b, parity)) return true;
     if ((spin & 63) == 0) {
       if (abort && *abort) return false;
-      const unsigned long long now = global_ns();
+      const long long now = clock64();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kTcWaitNs) return false;
+      if (now - t0 > kPtWaitCycles) return false;
     }
   }
 }
@@ -157,19 +158,35 @@ __device__ __forceinline__ bool pt_wait(uint64_t* b, uint32_t parity, const vola
 constexpr uint32_t kPtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t pt_desc_lo(const void* p, uint32_t lbo) { return ((smem_addr(p) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
 
-// D[tmem] (+)= A B over K = 16, A from shared memory or (ts) from TMEM.
-__device__ __forceinline__ void pt_mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A B over K = 16, A from shared memory or (ts) from TMEM; the
+// lane with `on` issues.  Each issue is predicated by itself: inside a branch
+// of one lane the operands would be moved to uniform registers one by one,
+// which a busy scheduler makes slower than the product (110 cycles against 64).
+__device__ __forceinline__ void pt_mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate, uint32_t on) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d_tmem),
-      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi)
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t accumulate, uint32_t on) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi)
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 db, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(kPtDescHi), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void pt_commit(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          smem_addr(bar)),
+      "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void pt_arrive(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}" ::"r"(smem_addr(bar)), "r"(on)
       : "memory");
 }
 #define HADQ_R32 \
@@ -693,45 +710,36 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     // The whole warp walks the schedule, one lane issues.  Descriptors and
     // TMEM addresses are sums of warp-uniform bases and constants (group and
     // stage unrolled), so that an issue costs no moves to uniform registers.
-    bool dead = false;
+    uint32_t on = elect_one();  // this lane issues, until a wait has run out
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!pt_wait(bar, parity, abort)) {
-        if (!dead && lane == 0) tc_give_up(&tl->abort, fault);
-        dead = true;
+        if (on) tc_give_up(&tl->abort, fault);
+        on = 0;
       }
     };
     const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtHalf);
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one() && !dead) tc_commit(bar);
-      __syncwarp();
-    };
+    auto commit = [&](uint64_t* bar) { pt_commit(bar, on); };
     auto mma_s = [&](auto M, auto STAGE) {  // S_m = Q_m K^T
       constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
       tc_fence_after();
-      if (elect_one() && !dead) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-          const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
-          pt_mma_ss(128 * m, qd + (m * (kPtMat >> 4) + o), kd + (st * (kPtMat >> 4) + o), kPtIdescQK, k > 0);
-        }
-        // The softmax reads what the key warps wrote beside the keys
-        // (exponents, cached bits) once S is there: this warp has seen their
-        // arrival and passes it on.  (They cannot wait for k_full themselves:
-        // it may be a phase further on by then.)
-        mbar_arrive(&tl->s_full[m]);
-        tc_commit(&tl->s_full[m]);
+      for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
+        pt_mma_ss(128 * m, qd + (m * (kPtMat >> 4) + o), kd + (st * (kPtMat >> 4) + o), kPtIdescQK, k > 0, on);
       }
-      __syncwarp();
+      // The softmax reads what the key warps wrote beside the keys (exponents,
+      // cached bits) once S is there: this warp has seen their arrival and
+      // passes it on.  (They cannot wait for k_full themselves: it may be a
+      // phase further on by then.)
+      pt_arrive(&tl->s_full[m], on);
+      commit(&tl->s_full[m]);
     };
     auto mma_o = [&](auto M, auto STAGE, bool add) {  // O_m (+)= P_m V
       constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
       tc_fence_after();
-      if (elect_one() && !dead) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k)
-          pt_mma_ts(256 + 128 * m, 128 * m + 64 + 8 * k, vd + (st * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV, k > 0 ? 1u : uint32_t(add));
-      }
-      __syncwarp();
+      for (uint32_t k = 0; k < 8; ++k)
+        pt_mma_ts(256 + 128 * m, 128 * m + 64 + 8 * k, vd + (st * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV, k > 0 ? 1u : uint32_t(add), on);
     };
     constexpr PtInt<0> c0{};
     constexpr PtInt<1> c1{};
@@ -781,7 +789,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       if (two) pu1 ^= 1;
     } while (it.warp_next(a, per));
     // every MMA is complete before TMEM is freed (passes at once normally)
-    if (!dead) (void)pt_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
+    if (on) (void)pt_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
+    __syncwarp();
     }
   }
 
