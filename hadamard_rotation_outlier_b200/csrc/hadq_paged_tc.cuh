@@ -8,9 +8,9 @@
 // eight tcgen05.mma of K = 16 each, all operands f16:
 //  * keys and values are codes times their scale over 2^e, e the exponent of
 //    the tile's largest scale, so both fill the f16 range from the top
-//    whatever the scales are.  A key is rounded once (scale in two f16 terms,
-//    fma), a value twice (scale and product): 11 bits, where the output has 8;
-//  * the rotated query is scaled by the exponent of its group's largest entry;
+//    whatever the scales are.  The scale and the product are rounded to
+//    f16: 11 bits, where the output has 8;
+//  * the rotated query is scaled by a bound of its group's largest entry;
 //  * the exponents come back as one multiplier per tile in the exponent's fma
 //    (scores) and as a summand of the softmax reference (values): with
 //    m >= max(score + e), a weight is 2^(score + e - m) <= 2^8, and l counts
@@ -35,8 +35,8 @@
 // straight code): with four instruction streams on an SM, fetching them cost
 // more than the work did (7400 cycles a tile with everything unrolled).
 // The columns of Q, K, V are stored in the order in which one mask finds
-// them, dim 8 c + (0, 4, 1, 5, 2, 6, 3, 7): scores do not change, and H_128 of
-// O is the same up to that order.
+// them (pt_column): scores do not change, and H_128 of O is the same up to
+// that order, a permutation of index bits.
 //
 // Bound: 4 * 128 * 256 * 128 flops per tile pair take 2048 cycles at the dense
 // f16 rate; the 2 * 128 * 128 exponentials take as long at 16 a cycle, and
@@ -121,9 +121,10 @@ struct PtIter {
 struct PtTail {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  int kexp[4], vexp[4];     // exponents of the last four tiles' scales
+  uint32_t info[4];         // of the last four tiles: exponents of the largest K scale (bits 0-7) and V
+                            // scale (8-15), whether every key is cached (16)
   uint32_t ok[4][4];        // keys of the tile that are cached (bit per key)
-  uint32_t red[2][4];       // group maxima of |q|
+  uint32_t red[2][4];       // group maxima of the rows' sums of |q|
   uint32_t dred[2][2][2][4];  // tile maxima of the scales: [role][parity][K, V][warp]
   uint32_t sgn[4];          // sign bits of the 128 columns
   int last[2];
@@ -226,9 +227,16 @@ template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // Registers of a thread: 640 threads launch with 96 each, 480 for the five
 // warps of a scheduler; two softmax warps, a key, a value and the MMA warp
-// get 2 * 144 + 2 * 72 + 48.
-constexpr int kPtRegsSoftmax = 144, kPtRegsCodes = 72, kPtRegsMma = 48;
+// get 2 * 136 + 2 * 80 + 48.
+constexpr int kPtRegsSoftmax = 136, kPtRegsCodes = 80, kPtRegsMma = 48;
 static_assert(2 * kPtRegsSoftmax + 2 * kPtRegsCodes + kPtRegsMma <= 5 * 96, "the launch's registers");
+
+// The column (of a group of eight) that a position of the converted operands
+// holds, and the other way round.
+template <int BITS>
+__host__ __device__ constexpr int pt_column(int p) { return BITS == 4 ? ((p & 1) << 2) | (p >> 1) : (p & 4) | ((p & 1) << 1) | ((p >> 1) & 1); }
+template <int BITS>
+__host__ __device__ constexpr int pt_position(int d) { return BITS == 4 ? ((d & 3) << 1) | (d >> 2) : (d & 4) | ((d & 1) << 1) | ((d >> 1) & 1); }
 
 template <uint32_t V>
 struct PtInt {
@@ -349,62 +357,170 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       }
     };
     int eq = 0;  // the group's queries are scaled by 2^eq
+    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
+    bool active = false;             // the group has rows in unit `it`
+    float M = -INFINITY, l = 0.f;
+    PtIter &it = tl->it[warp], &nx = tl->next[warp];
 
+    // Rows of 128 in two halves of 64: the butterfly between the halves as
+    // they are read, then H_64.  The raw row waits in its own place in shared
+    // memory.  The group's exponent comes from the rows' sums of |x|, which no
+    // rotated entry exceeds.
     auto load_queries = [&](const PtIter& u) {
-      float x[128];
       const int row = 128 * m + r;
-      if (row < u.ntok * a.g) {
-        const int tok = row / a.g, hh = row - tok * a.g;
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim);
+      uint8_t* dst = qs + m * kPtMat + r * 128;
+      auto chunk = [&](int c) { return reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (((c & 7) ^ (r & 7)) << 4)); };
+      float sum = 0.f;
+      const bool live = row < u.ntok * a.g;
+      const int tok = row / a.g, hh = row - tok * a.g;
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + (live ? int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim : 0));
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint4 w = __ldg(p + c);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[8 * c + 2 * k] = bf16lo(ww[k]);
-            x[8 * c + 2 * k + 1] = bf16hi(ww[k]);
-          }
-        }
-        if (a.signs) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(__float_as_uint(x[i]) ^ (((tl->sgn[i >> 5] >> (i & 31)) & 1u) << 31));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 128; ++i) x[i] = 0.f;
+      for (int c = 0; c < 16; ++c) {
+        uint4 w = live ? __ldg(p + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t sg = tl->sgn[c >> 2] >> (8 * (c & 3));  // signs of the eight columns
+        auto flip = [&](uint32_t x, int k) { return x ^ (((sg >> (2 * k)) & 1u) << 15) ^ (((sg >> (2 * k + 1)) & 1u) << 31); };
+        w = make_uint4(flip(w.x, 0), flip(w.y, 1), flip(w.z, 2), flip(w.w, 3));
+        sum += fabsf(bf16lo(w.x)) + fabsf(bf16hi(w.x)) + fabsf(bf16lo(w.y)) + fabsf(bf16hi(w.y)) + fabsf(bf16lo(w.z)) + fabsf(bf16hi(w.z)) +
+               fabsf(bf16lo(w.w)) + fabsf(bf16hi(w.w));
+        *chunk(c) = w;
       }
-      reg_fwht<128, 7>(x);
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 128; ++i) top = fmaxf(top, fabsf(x[i]));
-      const uint32_t wt = __reduce_max_sync(0xffffffffu, __float_as_uint(top * a.qmul));
+      const uint32_t wt = __reduce_max_sync(0xffffffffu, __float_as_uint(sum * a.qmul));
       if (lane == 0) tl->red[m][warp & 3] = wt;
       named_bar_sync(1 + m, 128);
       const uint32_t gt = max(max(tl->red[m][0], tl->red[m][1]), max(tl->red[m][2], tl->red[m][3]));
-      // largest entry to [2^13, 2^14); a group whose entries are all below
-      // 2^-100 counts as zero
+      // the bound to [2^14, 2^15); a group whose entries are all below 2^-100
+      // counts as zero
       const int ge = min(int(gt >> 23), 253);
       const bool zero = ge < 27;
-      eq = zero ? 0 : 140 - ge;
+      eq = zero ? 0 : 141 - ge;
       const float up = zero ? 0.f : a.qmul * pow2_clamped(eq);
-      uint8_t* dst = qs + m * kPtMat + r * 128;
+      auto half = [&](bool upper, uint32_t (&out)[32]) {
+        float y[64];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float* y = x + 8 * c;
-        const uint4 w = make_uint4(cvt_f16x2(y[0] * up, y[4] * up), cvt_f16x2(y[1] * up, y[5] * up), cvt_f16x2(y[2] * up, y[6] * up),
-                                   cvt_f16x2(y[3] * up, y[7] * up));
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (((c & 7) ^ (r & 7)) << 4)) = w;
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *chunk(c), w = *chunk(c + 8);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[8 * c + 2 * k] = upper ? bf16lo(vv[k]) - bf16lo(ww[k]) : bf16lo(vv[k]) + bf16lo(ww[k]);
+            y[8 * c + 2 * k + 1] = upper ? bf16hi(vv[k]) - bf16hi(ww[k]) : bf16hi(vv[k]) + bf16hi(ww[k]);
+          }
+        }
+        reg_fwht<64, 6>(y);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int c = 8 * (k >> 2), q = 2 * (k & 3);
+          out[k] = cvt_f16x2(y[c + pt_column<BITS>(q)] * up, y[c + pt_column<BITS>(q + 1)] * up);
+        }
+      };
+      uint32_t o0[32], o1[32];
+      half(false, o0);
+      half(true, o1);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        *chunk(c) = make_uint4(o0[4 * c], o0[4 * c + 1], o0[4 * c + 2], o0[4 * c + 3]);
+        *chunk(c + 8) = make_uint4(o1[4 * c], o1[4 * c + 1], o1[4 * c + 2], o1[4 * c + 3]);
       }
       fence_async_shared();
       named_bar_sync(1 + m, 128);  // tl->red has been read; the group's rows are written
       if (lane == 0) mbar_arrive(&tl->q_full[m]);
     };
 
-    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
-    bool active = false;             // the group has rows in unit `it`
-    float M = -INFINITY, l = 0.f;
-    PtIter &it = tl->it[warp], &nx = tl->next[warp];
+    // The unit's partial O to the workspace; the last CTA to come sums them up
+    // and leaves the total in TMEM.  Returns whether this one does.
+    auto join = [&]() {
+      const int row = 128 * m + r;
+      const int c0 = int(it.ustart / pc.quota), c1 = int((it.ustart + it.tl.count - 1) / pc.quota);
+      auto slot = [&](int x) { return 2 * int64_t(x) + (x == c0 ? 1 : 0); };
+      float4* po = reinterpret_cast<float4*>(a.part_o);
+      float2* pm = reinterpret_cast<float2*>(a.part_ml);
+      const int64_t mine = slot(int(blockIdx.x));
+      if (!dead) pm[mine * kPtRows + row] = make_float2(M, l);
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float o[32];
+        tmem_ld32(tO + 32 * q, o);
+        if (!dead) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            po[(mine * 32 + 8 * q + c) * kPtRows + row] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      }
+      __threadfence();
+      named_bar_sync(1 + m, 128);
+      if (r == 0) tl->last[m] = !dead && atomicAdd(a.counters + kPtCounterBase + 2 * c0 + m, 1u) == unsigned(c1 - c0);
+      named_bar_sync(1 + m, 128);
+      if (!tl->last[m]) return false;
+      __threadfence();
+      M = -INFINITY;
+      for (int x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(&pm[slot(x) * kPtRows + row]).x);
+      l = 0.f;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float o[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+#pragma unroll 1
+        for (int x = c0; x <= c1; ++x) {
+          const float2 ml = __ldcg(&pm[slot(x) * kPtRows + row]);
+          const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+          if (q == 0) l = fmaf(w, ml.y, l);
+          const float4* px = po + (slot(x) * 32 + 8 * q) * kPtRows + row;
+          float4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = __ldcg(px + c * kPtRows);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            o[4 * c] = fmaf(w, v[c].x, o[4 * c]);
+            o[4 * c + 1] = fmaf(w, v[c].y, o[4 * c + 1]);
+            o[4 * c + 2] = fmaf(w, v[c].z, o[4 * c + 2]);
+            o[4 * c + 3] = fmaf(w, v[c].w, o[4 * c + 3]);
+          }
+        }
+        uint32_t y[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(o[k]);
+        tmem_st32(tO + 32 * q, y);
+      }
+      tmem_wait_st();
+      if (r == 0) a.counters[kPtCounterBase + 2 * c0 + m] = 0u;  // ready for the next call
+      return true;
+    };
+
+    // Rotate back (halves as above), normalise, sign, store.
+    auto finish = [&]() {
+      const int row = 128 * m + r;
+      const bool store = row < it.ntok * a.g && !dead;
+      const float inv = l > 0.f ? a.inv_sqrt_dim * 0.0078125f / l : 0.f;  // values entered times 2^7
+      const int tok = row / a.g, hh = row - tok * a.g;
+      uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(it.rq.row0 + it.first + tok) * a.nqh + it.h * a.g + hh) * kPagedDim);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float y[64];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float w[32];
+          tmem_ld32(tO + 32 * q, *reinterpret_cast<float(*)[32]>(y + 32 * q));
+          tmem_ld32(tO + 64 + 32 * q, w);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[32 * q + k] = h ? y[32 * q + k] - w[k] : y[32 * q + k] + w[k];
+        }
+        reg_fwht<64, 6>(y);
+        if (store) {
+          const uint32_t sg[2] = {tl->sgn[2 * h], tl->sgn[2 * h + 1]};
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = cvt_bf16x2(y[8 * c + pt_position<BITS>(2 * k)] * inv, y[8 * c + pt_position<BITS>(2 * k + 1)] * inv) ^
+                     (((sg[c >> 2] >> (8 * (c & 3) + 2 * k)) & 1u) << 15) ^ (((sg[c >> 2] >> (8 * (c & 3) + 2 * k + 1)) & 1u) << 31);
+            dst[8 * h + c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    };
+
     for (bool more = true;;) {
       // ---- the next unit's queries, then the output of the unit just done ----
       const bool next_active = more && 128 * m < nx.ntok * a.g;
@@ -413,74 +529,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         wait(&tl->o_full[m], nu & 1);
         ++nu;
         tc_fence_after();
-        float o[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tO + 32 * c, *reinterpret_cast<float(*)[32]>(o + 32 * c));
+        if (it.whole() || join()) finish();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tl->o_empty[m]);
-        const int row = 128 * m + r;
-        bool store = row < it.ntok * a.g && !dead;
-        if (!it.whole()) {
-          const int c0 = int(it.ustart / pc.quota), c1 = int((it.ustart + it.tl.count - 1) / pc.quota);
-          auto slot = [&](int x) { return 2 * int64_t(x) + (x == c0 ? 1 : 0); };
-          float4* po = reinterpret_cast<float4*>(a.part_o);
-          float2* pm = reinterpret_cast<float2*>(a.part_ml);
-          const int64_t mine = slot(int(blockIdx.x));
-          if (!dead) {
-            pm[mine * kPtRows + row] = make_float2(M, l);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) po[(mine * 32 + c) * kPtRows + row] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-          }
-          __threadfence();
-          named_bar_sync(1 + m, 128);
-          if (r == 0) tl->last[m] = !dead && atomicAdd(a.counters + kPtCounterBase + 2 * c0 + m, 1u) == unsigned(c1 - c0);
-          named_bar_sync(1 + m, 128);
-          store = store && tl->last[m];
-          if (tl->last[m]) {
-            __threadfence();
-            M = -INFINITY;
-            for (int x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(&pm[slot(x) * kPtRows + row]).x);
-            l = 0.f;
-#pragma unroll
-            for (int k = 0; k < 128; ++k) o[k] = 0.f;
-            for (int x = c0; x <= c1; ++x) {
-              const float2 ml = __ldcg(&pm[slot(x) * kPtRows + row]);
-              const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-              l = fmaf(w, ml.y, l);
-              const float4* px = po + slot(x) * 32 * kPtRows + row;
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const float4 v = __ldcg(px + c * kPtRows);
-                o[4 * c] = fmaf(w, v.x, o[4 * c]);
-                o[4 * c + 1] = fmaf(w, v.y, o[4 * c + 1]);
-                o[4 * c + 2] = fmaf(w, v.z, o[4 * c + 2]);
-                o[4 * c + 3] = fmaf(w, v.w, o[4 * c + 3]);
-              }
-            }
-            if (r == 0) a.counters[kPtCounterBase + 2 * c0 + m] = 0u;  // ready for the next call
-          }
-        }
-        if (store) {
-          reg_fwht<128, 7>(o);
-          const float inv = l > 0.f ? a.inv_sqrt_dim * 0.0078125f / l : 0.f;  // values entered times 2^7
-          const int tok = row / a.g, hh = row - tok * a.g;
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(it.rq.row0 + it.first + tok) * a.nqh + it.h * a.g + hh) * kPagedDim);
-#pragma unroll
-          for (int k = 0; k < 128; ++k) o[k] *= inv;
-          if (a.signs) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k) {
-              const int dim = (k & ~7) | ((k & 1) << 2) | ((k & 6) >> 1);
-              o[k] = __uint_as_float(__float_as_uint(o[k]) ^ (((tl->sgn[dim >> 5] >> (dim & 31)) & 1u) << 31));
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float* y = o + 8 * c;  // dims 0, 4, 1, 5, 2, 6, 3, 7
-            dst[c] = make_uint4(cvt_bf16x2(y[0], y[2]), cvt_bf16x2(y[4], y[6]), cvt_bf16x2(y[1], y[3]), cvt_bf16x2(y[5], y[7]));
-          }
-        }
       }
       if (!more) break;
       __syncwarp();
@@ -498,15 +550,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         const int f_tok = it.first + 128 * m / a.g, l_tok = it.first + min(128 * m + 127, it.ntok * a.g - 1) / a.g;
         const int all_lim = a.causal ? off + f_tok + 1 : it.rq.len;
         const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
-        for (int i = it.i0; i < it.i1; ++i, ++n, ++ns) {
+        const int i0 = it.i0, i1 = it.i1, head = it.tl.head, from = it.tl.from - head;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i, ++n, ++ns) {
+          const int t0 = (i < head ? i : i + from) * kPtTile;
+          bool masked = t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low);
           wait(&tl->s_full[m], ns & 1);
           tc_fence_after();
-          const int ve = tl->vexp[n & 3];
-          const float f = pow2_clamped(tl->kexp[n & 3] - 134 - eq), vexp = float(ve - 127);
-          const uint4 ok = *reinterpret_cast<const uint4*>(tl->ok[n & 3]);
-          const int t0 = it.key0(i);
-          const bool full = (ok.x & ok.y & ok.z & ok.w) == 0xffffffffu;
-          if (!full || t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low)) {  // put -inf where a row sees nothing
+          const uint32_t info = tl->info[n & 3];
+          const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
+          masked |= (info >> 16) == 0;
+          if (masked) {  // put -inf where a row sees nothing
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const int tc = t0 + 32 * c;
@@ -541,7 +595,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             const float alpha = need ? exp2f(M - top) : 1.f;
             if (need) M = top;
             l *= alpha;
-            if (i > it.i0) {  // the previous tiles' products are complete: S came after them
+            if (i > i0) {  // the previous tiles' products are complete: S came after them
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 float o[32];
@@ -558,19 +612,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll 1
           for (int c = 1; c >= 0; --c) {  // the second half is in registers
             if (c == 0) tmem_ld64(tS, s);
+            float x[64];
+#pragma unroll
+            for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) fma2(x[k], x[k + 1], f, sub);
+#pragma unroll
+            for (int k = 0; k < 64; ++k) x[k] = exp2_ftz(x[k]);
             uint32_t p[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              float x = __uint_as_float(s[2 * k]), y = __uint_as_float(s[2 * k + 1]);
-              fma2(x, y, f, sub);
-              x = exp2_ftz(x);
-              y = exp2_ftz(y);
-              if (k & 1) sum2(l2, l3, x, y); else sum2(l0, l1, x, y);
-              p[k] = cvt_f16x2(x, y);
+              if (k & 1) sum2(l2, l3, x[2 * k], x[2 * k + 1]); else sum2(l0, l1, x[2 * k], x[2 * k + 1]);
+              p[k] = cvt_f16x2(x[2 * k], x[2 * k + 1]);
             }
             tmem_st32(tS + 64 + 32 * c, p);
           }
-          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(127 - ve), l);
+          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(254 - int((info >> 8) & 255u) - 127), l);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -667,35 +724,31 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       const int ke = min(max(int(max(max(dk[0], dk[1]), max(dk[2], dk[3])) >> 23), 27), 227);
       const int ve = min(max(int(max(max(dv[0], dv[1]), max(dv[2], dv[3])) >> 23), 27), 227);
       if (role == 0 && t == 0) {
-        tl->kexp[n & 3] = ke;
-        tl->vexp[n & 3] = ve;
+        const uint32_t (&o)[4] = tl->ok[n & 3];
+        tl->info[n & 3] = uint32_t(ke) | (uint32_t(ve) << 8) | ((o[0] & o[1] & o[2] & o[3]) == 0xffffffffu ? 1u << 16 : 0u);
       }
       const float up = pow2_clamped(134 - (role ? ve : ke));  // largest scale to [2^7, 2^8)
-      uint32_t hi[NG], lo[NG];
+      uint32_t sc[NG];  // rounded to f16: 11 bits
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        const float x = own[q] * up;
-        hi[q] = cvt_f16x2(x, x);
-        float h;
-        asm("{.reg .f16 l, h;\n mov.b32 {l, h}, %1;\n cvt.f32.f16 %0, l;}" : "=f"(h) : "r"(hi[q]));
-        lo[q] = cvt_f16x2(x - h, x - h);
-      }
+      for (int q = 0; q < NG; ++q) sc[q] = cvt_f16x2(own[q] * up, own[q] * up);
       uint8_t* dst = mat + s * kPtMat;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {  // eight columns; a used-up piece is refilled with the next tile's
         constexpr int CP = 16 / NV;   // chunks per piece
         const uint4 v = cur[c / CP];
         uint32_t p[4];
-        if constexpr (BITS == 4)
+        if constexpr (BITS == 4) {
           i4x4_to_f16_tokens((c & 3) == 0 ? v.x : (c & 3) == 1 ? v.y : (c & 3) == 2 ? v.z : v.w, p);
-        else
-          i8x8_to_f16_pairs((c & 1) ? v.z : v.x, (c & 1) ? v.w : v.y, p);
-        const int q = c * NG / 16;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t z = f16x2_mul(p[y], lo[q]);
-          asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[y]) : "r"(p[y]), "r"(hi[q]), "r"(z));
+        } else {
+          const uint32_t w0 = (c & 1) ? v.z : v.x, w1 = (c & 1) ? v.w : v.y;
+          // bytes with the sign bit flipped are code + 128: 1152 + code
+          p[0] = f16x2_sub((w0 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          p[1] = f16x2_sub(((w0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          p[2] = f16x2_sub((w1 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          p[3] = f16x2_sub(((w1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
         }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sc[c * NG / 16]);
         *reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (offs[c & 3] ^ ((c & 4) << 4))) = make_uint4(p[0], p[1], p[2], p[3]);
         if (c % CP == CP - 1) cur[c / CP] = piece(c / CP);
       }
@@ -760,21 +813,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       auto tile = [&](auto STAGE, auto OTHER, int i) {
         constexpr uint32_t st = decltype(STAGE)::value, ot = decltype(OTHER)::value;
         const bool next = i + 1 < tiles;
+        // what is usually there already first, the weights last
+        wait(&tl->v_full[st], (n >> 1) & 1);
+        if (next) wait(&tl->k_full[ot], ((n + 1) >> 1) & 1);
+        if (i == 0) wait(&tl->o_empty[0], pu0 ^ 1u);
         wait(&tl->p_full[0], pp0);
         pp0 ^= 1;
-        wait(&tl->v_full[st], (n >> 1) & 1);
-        if (i == 0) wait(&tl->o_empty[0], pu0 ^ 1u);
         mma_o(c0, STAGE, i > 0);
         if (next) {
-          wait(&tl->k_full[ot], ((n + 1) >> 1) & 1);
           mma_s(c0, OTHER);
         } else {
           commit(&tl->o_full[0]);
         }
         if (two) {
+          if (i == 0) wait(&tl->o_empty[1], pu1 ^ 1u);
           wait(&tl->p_full[1], pp1);
           pp1 ^= 1;
-          if (i == 0) wait(&tl->o_empty[1], pu1 ^ 1u);
           mma_o(c1, STAGE, i > 0);
           if (next) mma_s(c1, OTHER); else commit(&tl->o_full[1]);
         }
