@@ -29,8 +29,8 @@
 //    one tile ahead into registers, convert, scale and store them in the
 //    swizzled layout both products read (K: K-major, V: MN-major; the same
 //    bytes, and the same code);
-//  * warp 16 issues the MMAs.  Group 0's softmax runs under group 1's MMAs and
-//    the other way round.
+//  * warps 16 and 17 issue the MMAs of group 0 and 1.  Group 0's softmax runs
+//    under group 1's MMAs and the other way round.
 // The roles' loops are kept short (loops over quarters of a row instead of
 // straight code): with four instruction streams on an SM, fetching them cost
 // more than the work did (7400 cycles a tile with everything unrolled).
@@ -65,9 +65,9 @@ constexpr int kPtMat = 2 * kPtHalf;           // one f16 128 x 128 operand
 constexpr int kPtMaxCtas = 160;
 constexpr int kPtCounterBase = 1024;          // first of this kernel's arrival counters
 
-// Instruction descriptors: D float32, A and B f16, M = N = 128.
-constexpr uint32_t kPtIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kPtIdescPV = kPtIdescQK | (1u << 16);  // B MN-major
+// Instruction descriptors: D float32, A and B f16, M = 128.
+constexpr uint32_t kPtIdescQK = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);                  // N = 64 keys
+constexpr uint32_t kPtIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // N = 128 columns, B MN-major
 
 // A CTA's units and tiles in order.  Every warp walks its own copy, in shared
 // memory: in registers it would be spilled in the loops that matter.
@@ -119,7 +119,8 @@ struct PtIter {
 };
 
 struct PtTail {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2];  // by group, half of a tile's keys
+  uint64_t pv_done[2], o_full[2], o_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint32_t info[4];         // of the last four tiles: exponents of the largest K scale (bits 0-7) and V
                             // scale (8-15), whether every key is cached (16)
@@ -131,7 +132,7 @@ struct PtTail {
   uint32_t tmem_base;
   uint32_t abort;
   PagedPlanSmem plan;
-  PtIter it[17], next[8];  // by warp; the softmax warps also look one unit ahead
+  PtIter it[18], next[8];  // by warp; the softmax warps also look one unit ahead
 };
 static_assert(offsetof(PtTail, ok) % 16 == 0, "the cached bits are read as 16-byte vectors");
 __host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + size_t(6) * kPtMat + sizeof(PtTail); }
@@ -219,6 +220,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
                "r"(taddr)
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <int N>
@@ -294,14 +311,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tl->q_full[i], 4);
-      mbar_init(&tl->s_full[i], 2);
-      mbar_init(&tl->p_full[i], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&tl->s_full[i][h], 2);
+        mbar_init(&tl->p_full[i][h], 4);
+      }
+      mbar_init(&tl->pv_done[i], 1);
       mbar_init(&tl->o_full[i], 1);
       mbar_init(&tl->o_empty[i], 4);
       mbar_init(&tl->k_full[i], 4);
-      mbar_init(&tl->k_empty[i], 1);
+      mbar_init(&tl->k_empty[i], 2);
       mbar_init(&tl->v_full[i], 4);
-      mbar_init(&tl->v_empty[i], 1);
+      mbar_init(&tl->v_empty[i], 2);
     }
     tl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
   // of 128 columns each, at constant addresses.
   constexpr uint32_t tmem = 0;
 
-  if (warp < 17 && lane == 0) {
+  if (warp < 18 && lane == 0) {
     PtIter f;
     f.at = pc.at;
     f.end = pc.end;
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     regs_inc<kPtRegsSoftmax>();
     const int m = warp >> 2, r = tid & 127;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-    const uint32_t tS = tmem + lanes + uint32_t(128 * m), tO = tmem + lanes + uint32_t(256 + 128 * m);
+    const uint32_t tO = tmem + lanes + uint32_t(256 + 128 * m);
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!pt_wait(bar, parity, abort)) {
@@ -357,7 +377,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       }
     };
     int eq = 0;  // the group's queries are scaled by 2^eq
-    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
+    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, half tiles and units of this group
     bool active = false;             // the group has rows in unit `it`
     float M = -INFINITY, l = 0.f;
     PtIter &it = tl->it[warp], &nx = tl->next[warp];
@@ -552,86 +572,82 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
         const int i0 = it.i0, i1 = it.i1, head = it.tl.head, from = it.tl.from - head;
 #pragma unroll 1
-        for (int i = i0; i < i1; ++i, ++n, ++ns) {
-          const int t0 = (i < head ? i : i + from) * kPtTile;
-          bool masked = t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low);
-          wait(&tl->s_full[m], ns & 1);
+        for (int j = 2 * i0; j < 2 * i1; ++j, ++ns) {  // half tiles of 64 keys
+          const int h = j & 1, i = j >> 1;
+          const int t0 = (i < head ? i : i + from) * kPtTile + 64 * h;
+          const uint32_t tS = tmem + lanes + uint32_t(128 * m + 64 * h);
+          bool masked = t0 + 64 > all_lim || (a.window > 0 && t0 < all_low);
+          wait(&tl->s_full[m][h], (ns >> 1) & 1);
           tc_fence_after();
           const uint32_t info = tl->info[n & 3];
+          uint32_t s[64];
+          tmem_ld64(tS, s);
           const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
           masked |= (info >> 16) == 0;
-          if (masked) {  // put -inf where a row sees nothing
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+          if (masked) {  // -inf where a row sees nothing
+            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
+            uint32_t see[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
               const int tc = t0 + 32 * c;
-              auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
-              uint32_t see = tl->ok[n & 3][c] & below(lim - tc);
-              if (a.window > 0) see &= ~below(low - tc) | below(a.sinks - tc);
-              float x[32];
-              tmem_ld32(tS + 32 * c, x);
-              uint32_t y[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = (see >> k) & 1u ? __float_as_uint(x[k]) : 0xff800000u;
-              tmem_st32(tS + 32 * c, y);
+              see[c] = tl->ok[n & 3][2 * h + c] & below(lim - tc);
+              if (a.window > 0) see[c] &= ~below(low - tc) | below(a.sinks - tc);
             }
-            tmem_wait_st();
-          }
-          uint32_t s[64];
-          float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld64(tS + 64 * c, s);
 #pragma unroll
-            for (int k = 0; k < 64; k += 8) {
-              top0 = max3(top0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-              top1 = max3(top1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-              top2 = max3(top2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
-              top3 = max3(top3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
-            }
+            for (int k = 0; k < 64; ++k)
+              if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xff800000u;
           }
+          n += h;
+          float x[64];
+#pragma unroll
+          for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
+          float top0 = x[0], top1 = x[1], top2 = x[2], top3 = x[3];
+#pragma unroll
+          for (int k = 4; k < 60; k += 8) {
+            top0 = max3(top0, x[k], x[k + 1]);
+            top1 = max3(top1, x[k + 2], x[k + 3]);
+            top2 = max3(top2, x[k + 4], x[k + 5]);
+            top3 = max3(top3, x[k + 6], x[k + 7]);
+          }
+          top0 = max3(top0, x[60], x[61]);
+          top1 = max3(top1, x[62], x[63]);
           const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), f, vexp);
           const bool need = top > M + kAttnSlack;
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? exp2f(M - top) : 1.f;
             if (need) M = top;
             l *= alpha;
-            if (i > i0) {  // the previous tiles' products are complete: S came after them
+            if (j > 2 * i0) {
+              wait(&tl->pv_done[m], (ns - 1) & 1);  // the half before; S came after the one before that
+              tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float o[32];
-                tmem_ld32(tO + 32 * c, o);
-                uint32_t y[32];
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * c, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(o[k] * alpha);
-                tmem_st32(tO + 32 * c, y);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st16(tO + 16 * c, o);
               }
             }
           }
           const float sub = M == -INFINITY ? 0.f : vexp - M;
           float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll 1
-          for (int c = 1; c >= 0; --c) {  // the second half is in registers
-            if (c == 0) tmem_ld64(tS, s);
-            float x[64];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
+          for (int k = 0; k < 64; k += 2) fma2(x[k], x[k + 1], f, sub);
 #pragma unroll
-            for (int k = 0; k < 64; k += 2) fma2(x[k], x[k + 1], f, sub);
+          for (int k = 0; k < 64; ++k) x[k] = exp2_ftz(x[k]);
+          uint32_t p[32];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) x[k] = exp2_ftz(x[k]);
-            uint32_t p[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (k & 1) sum2(l2, l3, x[2 * k], x[2 * k + 1]); else sum2(l0, l1, x[2 * k], x[2 * k + 1]);
-              p[k] = cvt_f16x2(x[2 * k], x[2 * k + 1]);
-            }
-            tmem_st32(tS + 64 + 32 * c, p);
+          for (int k = 0; k < 32; ++k) {
+            if (k & 1) sum2(l2, l3, x[2 * k], x[2 * k + 1]); else sum2(l0, l1, x[2 * k], x[2 * k + 1]);
+            p[k] = cvt_f16x2(x[2 * k], x[2 * k + 1]);
           }
-          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(254 - int((info >> 8) & 255u) - 127), l);
+          tmem_st32(tS + 32, p);
+          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(127 - int((info >> 8) & 255u)), l);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tl->p_full[m]);
+          if (lane == 0) mbar_arrive(&tl->p_full[m][h]);
         }
       } else {
         n += it.i1 - it.i0;
@@ -688,11 +704,13 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         vscl[q] = have ? __ldg(a.v_scales + row * NG + q) : 0.f;
       }
     };
-    auto piece = [&](int x) { return have ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u); };
+    auto load = [&]() {
+#pragma unroll
+      for (int x = 0; x < NV; ++x) cur[x] = have ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+    };
     find();
     locate();
-#pragma unroll
-    for (int x = 0; x < NV; ++x) cur[x] = piece(x);
+    load();
     find();
     const uint32_t offs[4] = {uint32_t((0 ^ (t & 7)) << 4), uint32_t((1 ^ (t & 7)) << 4), uint32_t((2 ^ (t & 7)) << 4), uint32_t((3 ^ (t & 7)) << 4)};
     const uint32_t total = uint32_t(pc.end - pc.at);
@@ -732,34 +750,48 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
       for (int q = 0; q < NG; ++q) sc[q] = cvt_f16x2(own[q] * up, own[q] * up);
       uint8_t* dst = mat + s * kPtMat;
+#pragma unroll 1
+      for (int c4 = 0; c4 < 4; ++c4) {  // 32 columns: the front pieces of cur, which then moves up
+        const uint32_t sq = NG == 2 && c4 >= 2 ? sc[NG - 1] : sc[0];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {  // eight columns; a used-up piece is refilled with the next tile's
-        constexpr int CP = 16 / NV;   // chunks per piece
-        const uint4 v = cur[c / CP];
-        uint32_t p[4];
-        if constexpr (BITS == 4) {
-          i4x4_to_f16_tokens((c & 3) == 0 ? v.x : (c & 3) == 1 ? v.y : (c & 3) == 2 ? v.z : v.w, p);
-        } else {
-          const uint32_t w0 = (c & 1) ? v.z : v.x, w1 = (c & 1) ? v.w : v.y;
-          // bytes with the sign bit flipped are code + 128: 1152 + code
-          p[0] = f16x2_sub((w0 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-          p[1] = f16x2_sub(((w0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-          p[2] = f16x2_sub((w1 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-          p[3] = f16x2_sub(((w1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[4];
+          if constexpr (BITS == 4) {
+            i4x4_to_f16_tokens(x == 0 ? cur[0].x : x == 1 ? cur[0].y : x == 2 ? cur[0].z : cur[0].w, p);
+          } else {
+            const uint4 v = cur[x >> 1];
+            const uint32_t w0 = (x & 1) ? v.z : v.x, w1 = (x & 1) ? v.w : v.y;
+            // bytes with the sign bit flipped are code + 128: 1152 + code
+            p[0] = f16x2_sub((w0 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            p[1] = f16x2_sub(((w0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            p[2] = f16x2_sub((w1 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            p[3] = f16x2_sub(((w1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sq);
+          *reinterpret_cast<uint4*>(dst + (offs[x] ^ ((c4 & 1) << 6))) = make_uint4(p[0], p[1], p[2], p[3]);
         }
+        constexpr int STEP = NV / 4;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sc[c * NG / 16]);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (offs[c & 3] ^ ((c & 4) << 4))) = make_uint4(p[0], p[1], p[2], p[3]);
-        if (c % CP == CP - 1) cur[c / CP] = piece(c / CP);
+        for (int x = 0; x + STEP < NV; ++x) cur[x] = cur[x + STEP];
+        if constexpr (NG == 4) {
+          sc[0] = sc[1];
+          sc[1] = sc[2];
+          sc[2] = sc[3];
+        }
+        if (c4 == 1) dst += kPtHalf;
       }
+      load();
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
     }
   } else {
     regs_dec<kPtRegsMma>();
-    if (warp == 16) {
+    if (warp < 18) {
     // ================================================================== MMAs
+    // One warp per group: the control code between the issues takes as long as
+    // the products (one warp for both was busy 4500 of 5400 cycles a tile).
     // The whole warp walks the schedule, one lane issues.  Descriptors and
     // TMEM addresses are sums of warp-uniform bases and constants (group and
     // stage unrolled), so that an issue costs no moves to uniform registers.
@@ -771,76 +803,62 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       }
     };
     const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtHalf);
-    auto commit = [&](uint64_t* bar) { pt_commit(bar, on); };
-    auto mma_s = [&](auto M, auto STAGE) {  // S_m = Q_m K^T
-      constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
-      tc_fence_after();
-#pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-        const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
-        pt_mma_ss(128 * m, qd + (m * (kPtMat >> 4) + o), kd + (st * (kPtMat >> 4) + o), kPtIdescQK, k > 0, on);
-      }
-      // The softmax reads what the key warps wrote beside the keys (exponents,
-      // cached bits) once S is there: this warp has seen their arrival and
-      // passes it on.  (They cannot wait for k_full themselves: it may be a
-      // phase further on by then.)
-      pt_arrive(&tl->s_full[m], on);
-      commit(&tl->s_full[m]);
-    };
-    auto mma_o = [&](auto M, auto STAGE, bool add) {  // O_m (+)= P_m V
-      constexpr uint32_t m = decltype(M)::value, st = decltype(STAGE)::value;
-      tc_fence_after();
-#pragma unroll
-      for (uint32_t k = 0; k < 8; ++k)
-        pt_mma_ts(256 + 128 * m, 128 * m + 64 + 8 * k, vd + (st * (kPtMat >> 4) + k * (2048 >> 4)), kPtIdescPV, k > 0 ? 1u : uint32_t(add), on);
-    };
-    constexpr PtInt<0> c0{};
-    constexpr PtInt<1> c1{};
-    PtIter& it = tl->it[16];
-    uint32_t n = 0, pu0 = 0, pu1 = 0, pp0 = 0, pp1 = 0;  // parities of the groups' units and tiles
+    PtIter& it = tl->it[warp];
+    const int m = warp - 16;
+    const uint32_t qm = qd + uint32_t(m) * (kPtMat >> 4), sm = uint32_t(128 * m), om = uint32_t(256 + 128 * m);
+    uint32_t n = 0, pu = 0, pp = 0;  // tiles of the CTA; parities of the group's units and tiles
     do {
-      const bool two = __shfl_sync(0xffffffffu, int(it.ntok * a.g > 128), 0);
-      const int tiles = __shfl_sync(0xffffffffu, it.i1 - it.i0, 0);
-      wait(&tl->q_full[0], pu0);
-      wait(&tl->k_full[n & 1], (n >> 1) & 1);
-      if (n & 1) mma_s(c0, c1); else mma_s(c0, c0);
-      if (two) {
-        wait(&tl->q_full[1], pu1);
-        if (n & 1) mma_s(c1, c1); else mma_s(c1, c0);
-      }
-      commit(&tl->k_empty[n & 1]);
-      // Tile i: O += P V, then S of tile i + 1, for either group.
-      auto tile = [&](auto STAGE, auto OTHER, int i) {
-        constexpr uint32_t st = decltype(STAGE)::value, ot = decltype(OTHER)::value;
-        const bool next = i + 1 < tiles;
-        // what is usually there already first, the weights last
-        wait(&tl->v_full[st], (n >> 1) & 1);
-        if (next) wait(&tl->k_full[ot], ((n + 1) >> 1) & 1);
-        if (i == 0) wait(&tl->o_empty[0], pu0 ^ 1u);
-        wait(&tl->p_full[0], pp0);
-        pp0 ^= 1;
-        mma_o(c0, STAGE, i > 0);
-        if (next) {
-          mma_s(c0, OTHER);
-        } else {
-          commit(&tl->o_full[0]);
-        }
-        if (two) {
-          if (i == 0) wait(&tl->o_empty[1], pu1 ^ 1u);
-          wait(&tl->p_full[1], pp1);
-          pp1 ^= 1;
-          mma_o(c1, STAGE, i > 0);
-          if (next) mma_s(c1, OTHER); else commit(&tl->o_full[1]);
-        }
-        commit(&tl->v_empty[st]);
-        if (next) commit(&tl->k_empty[ot]);
-      };
+      const bool active = it.ntok * a.g > 128 * m;
+      const int halves = 2 * (it.i1 - it.i0);
+      if (!active) {  // the stages pass unused
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i, ++n) {
-        if (n & 1) tile(c1, c0, i); else tile(c0, c1, i);
+        for (int i = 0; i < halves; i += 2, ++n) {
+          wait(&tl->k_full[n & 1], (n >> 1) & 1);
+          pt_arrive(&tl->k_empty[n & 1], on);
+          wait(&tl->v_full[n & 1], (n >> 1) & 1);
+          pt_arrive(&tl->v_empty[n & 1], on);
+        }
+        continue;
       }
-      pu0 ^= 1;
-      if (two) pu1 ^= 1;
+      // Step j: O += P V of half j, then S of half j + 2 in P's place.
+#pragma unroll 1
+      for (int j = -2; j < halves; ++j) {
+        const uint32_t h = j & 1;
+        const uint32_t vt = n + uint32_t((j >> 1)), kt = vt + 1;  // tiles of the two halves
+        if (j >= 0) {
+          if (h == 0) wait(&tl->v_full[vt & 1], (vt >> 1) & 1);
+          if (j == 0) wait(&tl->o_empty[m], pu ^ 1u);
+          wait(&tl->p_full[m][h], pp);
+          pp ^= h;
+          tc_fence_after();
+          const uint32_t av = sm + 64 * h + 32, bv = vd + (vt & 1) * (kPtMat >> 4) + h * (8192 >> 4);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) pt_mma_ts(om, av + 8 * k, bv + k * (2048 >> 4), kPtIdescPV, k > 0 ? 1u : uint32_t(j > 0), on);
+          pt_commit(&tl->pv_done[m], on);
+          if (h) pt_commit(&tl->v_empty[vt & 1], on);
+        }
+        if (j + 2 < halves) {
+          if (j == -2) wait(&tl->q_full[m], pu);
+          if (h == 0) wait(&tl->k_full[kt & 1], (kt >> 1) & 1);
+          tc_fence_after();
+          const uint32_t bk = kd + (kt & 1) * (kPtMat >> 4) + h * (8192 >> 4);
+#pragma unroll
+          for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
+            pt_mma_ss(sm + 64 * h, qm + o, bk + o, kPtIdescQK, k > 0, on);
+          }
+          // The softmax reads what the key warps wrote beside the keys
+          // (exponents, cached bits) once S is there: this warp has seen their
+          // arrival and passes it on.  (They cannot wait for k_full
+          // themselves: it may be a phase further on by then.)
+          pt_arrive(&tl->s_full[m][h], on);
+          pt_commit(&tl->s_full[m][h], on);
+          if (h) pt_commit(&tl->k_empty[kt & 1], on);
+        }
+      }
+      pt_commit(&tl->o_full[m], on);
+      n += uint32_t(halves) / 2;
+      pu ^= 1;
     } while (it.warp_next(a, per));
     // every MMA is complete before TMEM is freed (passes at once normally)
     if (on) (void)pt_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
