@@ -244,8 +244,8 @@ template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // Registers of a thread: 640 threads launch with 96 each, 480 for the five
 // warps of a scheduler; two softmax warps, a key, a value and the MMA warp
-// get 2 * 136 + 2 * 80 + 48.
-constexpr int kPtRegsSoftmax = 136, kPtRegsCodes = 80, kPtRegsMma = 48;
+// get 2 * 152 + 2 * 64 + 48.
+constexpr int kPtRegsSoftmax = 152, kPtRegsCodes = 64, kPtRegsMma = 48;
 static_assert(2 * kPtRegsSoftmax + 2 * kPtRegsCodes + kPtRegsMma <= 5 * 96, "the launch's registers");
 
 // The column (of a group of eight) that a position of the converted operands
@@ -580,23 +580,25 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           wait(&tl->s_full[m][h], (ns >> 1) & 1);
           tc_fence_after();
           const uint32_t info = tl->info[n & 3];
+          masked |= (info >> 16) == 0;
+          if (masked) {  // put -inf where a row sees nothing
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int tc = t0 + 16 * c;
+              auto below = [](int x) { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1u; };
+              uint32_t see = (tl->ok[n & 3][2 * h + (c >> 1)] >> (16 * (c & 1))) & below(lim - tc);
+              if (a.window > 0) see &= ~below(low - tc) | below(a.sinks - tc);
+              uint32_t y[16];
+              tmem_ld16(tS + 16 * c, y);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) y[k] = (see >> k) & 1u ? y[k] : 0xff800000u;
+              tmem_st16(tS + 16 * c, y);
+            }
+            tmem_wait_st();
+          }
           uint32_t s[64];
           tmem_ld64(tS, s);
           const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
-          masked |= (info >> 16) == 0;
-          if (masked) {  // -inf where a row sees nothing
-            auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; };
-            uint32_t see[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int tc = t0 + 32 * c;
-              see[c] = tl->ok[n & 3][2 * h + c] & below(lim - tc);
-              if (a.window > 0) see[c] &= ~below(low - tc) | below(a.sinks - tc);
-            }
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xff800000u;
-          }
           n += h;
           float x[64];
 #pragma unroll
