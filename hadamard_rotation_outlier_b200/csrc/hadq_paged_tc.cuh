@@ -25,8 +25,10 @@
 //    second half.  They also rotate the next unit's queries into shared memory
 //    (H_128 in registers) before they finish a unit (rotate back, normalise,
 //    store);
-//  * warps 8-11 (keys) and 12-15 (values): a cached row per thread: load codes
-//    one tile ahead into registers, convert, scale and store them in the
+//  * warps 18 and 19 plan tiles ahead: the rows' places in the pool, their
+//    scales and the largest one's exponent;
+//  * warps 8-11 (keys) and 12-15 (values): half a cached row per thread: load
+//    codes one tile ahead into registers, convert, scale and store them in the
 //    swizzled layout both products read (K: K-major, V: MN-major; the same
 //    bytes, and the same code);
 //  * warps 16 and 17 issue the MMAs of group 0 and 1.  Group 0's softmax runs
@@ -59,9 +61,13 @@ namespace hadq {
 
 constexpr int kPtThreads = 640;
 constexpr int kPtRows = 256;  // query rows per unit
-constexpr int kPtTile = 128;  // keys per tile
-constexpr int kPtHalf = 128 * 128;            // bytes of 64 columns x 128 rows
-constexpr int kPtMat = 2 * kPtHalf;           // one f16 128 x 128 operand
+constexpr int kPtTile = 64;   // keys per tile
+constexpr int kPtStages = 4;  // tiles of K, and of V, in shared memory
+constexpr int kPtHalf = 128 * 128;            // bytes of 64 columns of a group's queries
+constexpr int kPtMat = 2 * kPtHalf;           // a group's queries in f16
+constexpr int kPtKvHalf = 64 * 128, kPtKv = 2 * kPtKvHalf;  // the same of a tile of K or V
+constexpr int kPtPlans = 4;   // tiles whose rows and scales are worked out ahead
+constexpr int kPtInfos = 16;  // tiles whose info the softmax may still need: 2 ahead of it in S, 4 in K, 4 planned
 constexpr int kPtMaxCtas = 160;
 constexpr int kPtCounterBase = 1024;          // first of this kernel's arrival counters
 
@@ -119,23 +125,24 @@ struct PtIter {
 };
 
 struct PtTail {
-  uint64_t q_full[2], s_full[2][2], p_full[2][2];  // by group, half of a tile's keys
+  uint64_t q_full[2], s_full[2][2], p_full[2][2];  // by group, S buffer
   uint64_t pv_done[2], o_full[2], o_empty[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint32_t info[4];         // of the last four tiles: exponents of the largest K scale (bits 0-7) and V
-                            // scale (8-15), whether every key is cached (16)
-  uint32_t ok[4][4];        // keys of the tile that are cached (bit per key)
+  uint64_t k_full[kPtStages], k_empty[kPtStages], v_full[kPtStages], v_empty[kPtStages];
+  uint64_t plan_full[kPtPlans], plan_empty[kPtPlans];
+  uint32_t info[kPtInfos];   // of the last tiles: exponents of the largest K scale (bits 0-7) and V scale
+                             // (8-15), whether every key is cached (16)
+  uint32_t ok[kPtInfos][2];  // the tile's keys that are cached
+  uint32_t row[kPtPlans][kPtTile];       // rows of the tile's keys in the pool, ~0: not cached
+  uint32_t scale[kPtPlans][2][4][kPtTile];  // K and V scales over 2^e as f16 pairs, by group
   uint32_t red[2][4];       // group maxima of the rows' sums of |q|
-  uint32_t dred[2][2][2][4];  // tile maxima of the scales: [role][parity][K, V][warp]
   uint32_t sgn[4];          // sign bits of the 128 columns
   int last[2];
   uint32_t tmem_base;
   uint32_t abort;
   PagedPlanSmem plan;
-  PtIter it[18], next[8];  // by warp; the softmax warps also look one unit ahead
+  PtIter it[20], next[8];  // by warp; the softmax warps also look one unit ahead
 };
-static_assert(offsetof(PtTail, ok) % 16 == 0, "the cached bits are read as 16-byte vectors");
-__host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + size_t(6) * kPtMat + sizeof(PtTail); }
+__host__ __device__ constexpr size_t pt_smem_bytes() { return 1024 + 2 * size_t(kPtMat) + 2 * size_t(kPtStages) * kPtKv + sizeof(PtTail); }
 
 // Wait for the phase of `parity`; false after about a second, or as soon as
 // another role has given up.  The clock (the SM's own, which is read at once)
@@ -292,9 +299,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
   extern __shared__ uint8_t pt_smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = base;                // [group][half][128 rows][128 bytes]
-  uint8_t* ks = base + 2 * kPtMat;   // [stage][half][128 keys][128 bytes]
-  uint8_t* vs = base + 4 * kPtMat;
-  PtTail* tl = reinterpret_cast<PtTail*>(base + 6 * kPtMat);
+  uint8_t* ks = base + 2 * kPtMat;   // [stage][half][64 keys][128 bytes]
+  uint8_t* vs = ks + kPtStages * kPtKv;
+  PtTail* tl = reinterpret_cast<PtTail*>(vs + kPtStages * kPtKv);
   const volatile uint32_t* abort = &tl->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = kPtRows / a.g;  // query tokens per unit
@@ -318,10 +325,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       mbar_init(&tl->pv_done[i], 1);
       mbar_init(&tl->o_full[i], 1);
       mbar_init(&tl->o_empty[i], 4);
+    }
+    for (int i = 0; i < kPtStages; ++i) {
       mbar_init(&tl->k_full[i], 4);
       mbar_init(&tl->k_empty[i], 2);
       mbar_init(&tl->v_full[i], 4);
       mbar_init(&tl->v_empty[i], 2);
+    }
+    for (int i = 0; i < kPtPlans; ++i) {
+      mbar_init(&tl->plan_full[i], 1);
+      mbar_init(&tl->plan_empty[i], 8);
     }
     tl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
   // of 128 columns each, at constant addresses.
   constexpr uint32_t tmem = 0;
 
-  if (warp < 18 && lane == 0) {
+  if (lane == 0) {
     PtIter f;
     f.at = pc.at;
     f.end = pc.end;
@@ -377,7 +390,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       }
     };
     int eq = 0;  // the group's queries are scaled by 2^eq
-    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, half tiles and units of this group
+    uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
     bool active = false;             // the group has rows in unit `it`
     float M = -INFINITY, l = 0.f;
     PtIter &it = tl->it[warp], &nx = tl->next[warp];
@@ -572,21 +585,21 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
         const int i0 = it.i0, i1 = it.i1, head = it.tl.head, from = it.tl.from - head;
 #pragma unroll 1
-        for (int j = 2 * i0; j < 2 * i1; ++j, ++ns) {  // half tiles of 64 keys
-          const int h = j & 1, i = j >> 1;
-          const int t0 = (i < head ? i : i + from) * kPtTile + 64 * h;
-          const uint32_t tS = tmem + lanes + uint32_t(128 * m + 64 * h);
-          bool masked = t0 + 64 > all_lim || (a.window > 0 && t0 < all_low);
+        for (int i = i0; i < i1; ++i, ++ns, ++n) {
+          const int t0 = (i < head ? i : i + from) * kPtTile;
+          const uint32_t h = ns & 1;  // S buffer
+          const uint32_t tS = tmem + lanes + uint32_t(128 * m) + 64 * h;
+          bool masked = t0 + kPtTile > all_lim || (a.window > 0 && t0 < all_low);
           wait(&tl->s_full[m][h], (ns >> 1) & 1);
           tc_fence_after();
-          const uint32_t info = tl->info[n & 3];
+          const uint32_t info = tl->info[n % kPtInfos];
           masked |= (info >> 16) == 0;
           if (masked) {  // put -inf where a row sees nothing
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const int tc = t0 + 16 * c;
               auto below = [](int x) { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1u; };
-              uint32_t see = (tl->ok[n & 3][2 * h + (c >> 1)] >> (16 * (c & 1))) & below(lim - tc);
+              uint32_t see = (tl->ok[n % kPtInfos][c >> 1] >> (16 * (c & 1))) & below(lim - tc);
               if (a.window > 0) see &= ~below(low - tc) | below(a.sinks - tc);
               uint32_t y[16];
               tmem_ld16(tS + 16 * c, y);
@@ -599,7 +612,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           uint32_t s[64];
           tmem_ld64(tS, s);
           const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
-          n += h;
           float x[64];
 #pragma unroll
           for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
@@ -619,8 +631,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             const float alpha = need ? exp2f(M - top) : 1.f;
             if (need) M = top;
             l *= alpha;
-            if (j > 2 * i0) {
-              wait(&tl->pv_done[m], (ns - 1) & 1);  // the half before; S came after the one before that
+            if (i > i0) {
+              wait(&tl->pv_done[m], (ns - 1) & 1);  // the tile before; S came after the one before that
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {
@@ -660,12 +672,13 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     // ======================================================= keys and values
     regs_dec<kPtRegsCodes>();
     const int role = (warp - 8) >> 2;  // 0: keys, 1: values
-    const int t = tid & 127, w = warp & 3;
-    constexpr int RB = 16 * BITS, NV = RB / 16;  // 16-byte pieces per row
-    const uint8_t* codes = role ? a.v_codes : a.k_codes;
+    const int t = tid & 127, key = t >> 1, part = t & 1;  // two threads per row, 64 columns each
+    constexpr int RB = 16 * BITS, NV = RB / 32;           // 16-byte pieces per half row
+    constexpr int NS = NG == 4 ? 2 : 1;                   // scales per half row
+    const uint8_t* codes = (role ? a.v_codes : a.k_codes) + part * (RB / 2);
     uint64_t* full = role ? tl->v_full : tl->k_full;
     uint64_t* empty = role ? tl->v_empty : tl->k_empty;
-    uint8_t* mat = (role ? vs : ks) + t * 128;
+    uint8_t* mat = (role ? vs : ks) + part * kPtKvHalf + key * 128;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!pt_wait(bar, parity, abort)) {
@@ -673,88 +686,34 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         dead = true;
       }
     };
-    // The iterator runs ahead of the tile in work: page ids by two tiles,
-    // codes and scales by one.
-    PtIter& it = tl->it[warp];
-    int i = it.i0;
-    bool more = true;
-    int page = -1, where = 0;  // of the tile to load next: this row's page, head and offset in it
-    int hd = 0;
-    auto find = [&]() {
-      page = -1;
-      if (!more) return;
-      const int pos = it.key0(i) + t;
-      hd = it.h;
-      where = pos & ((1 << a.page_log2) - 1);
-      if (pos < it.tl.kv_end) page = __ldg(a.table + int64_t(it.b) * a.max_pages + (pos >> a.page_log2));
-      if (++i == it.i1) {
-        more = it.warp_next(a, per);
-        i = it.i0;
-      }
-    };
     uint4 cur[NV];
-    float kscl[NG], vscl[NG];
-    bool have = false;           // the next row to load is cached
-    const uint4* src = nullptr;  // its codes
-    auto locate = [&]() {        // the found row: its scales now, its codes piece by piece
-      have = unsigned(page) < unsigned(a.n_pages);
-      const int64_t row = have ? ((int64_t(page) * a.nkv + hd) << a.page_log2) + where : 0;
-      src = reinterpret_cast<const uint4*>(codes + row * RB);
+    // The codes of tile n's row, once it is planned.  The second threads of
+    // the rows take their eight-column pieces four further on (mod 8) than the
+    // first: the four rows x two halves that a 128-bit store pass covers then
+    // lie in different banks.
+    auto load = [&](uint32_t n) {
+      wait(&tl->plan_full[n % kPtPlans], (n / kPtPlans) & 1);
+      const uint32_t row = tl->row[n % kPtPlans][key];
+      const uint4* src = reinterpret_cast<const uint4*>(codes + int64_t(row) * RB);
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        kscl[q] = have ? __ldg(a.k_scales + row * NG + q) : 0.f;
-        vscl[q] = have ? __ldg(a.v_scales + row * NG + q) : 0.f;
-      }
+      for (int x = 0; x < NV; ++x) cur[x] = row != ~0u && !dead ? __ldg(src + (x ^ (part * (NV / 2)))) : make_uint4(0u, 0u, 0u, 0u);
     };
-    auto load = [&]() {
-#pragma unroll
-      for (int x = 0; x < NV; ++x) cur[x] = have ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    find();
-    locate();
-    load();
-    find();
-    const uint32_t offs[4] = {uint32_t((0 ^ (t & 7)) << 4), uint32_t((1 ^ (t & 7)) << 4), uint32_t((2 ^ (t & 7)) << 4), uint32_t((3 ^ (t & 7)) << 4)};
+    load(0);
+    const uint32_t sw = uint32_t((key & 7) ^ (part << 2)) << 4;
     const uint32_t total = uint32_t(pc.end - pc.at);
 #pragma unroll 1
     for (uint32_t n = 0; n < total; ++n) {
-      const int s = n & 1;
-      const uint32_t ph = (n >> 1) & 1;
-      // exponents of the tile's largest scales
-      float kt = 0.f, vt = 0.f, own[NG];
+      const int st = n & (kPtStages - 1);
+      uint32_t sc[NS];
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        const float x = clean_scale(kscl[q]), y = clean_scale(vscl[q]);
-        kt = fmaxf(kt, x);
-        vt = fmaxf(vt, y);
-        own[q] = role ? y : x;
+      for (int q = 0; q < NS; ++q) {  // (in the order of the pieces)
+        const int grp = NG == 1 ? 0 : NG == 2 ? part : 2 * part + (q ^ part);
+        sc[q] = tl->scale[n % kPtPlans][role][grp][key];
       }
-      const uint32_t kw = __reduce_max_sync(0xffffffffu, __float_as_uint(kt)), vw = __reduce_max_sync(0xffffffffu, __float_as_uint(vt));
-      const uint32_t okw = __ballot_sync(0xffffffffu, have);
-      if (lane == 0) {
-        tl->dred[role][s][0][w] = kw;
-        tl->dred[role][s][1][w] = vw;
-      }
-      locate();  // the next tile's rows
-      find();
-      wait(&empty[s], ph ^ 1u);
-      if (role == 0 && lane == 0) tl->ok[n & 3][w] = okw;
-      named_bar_sync(3 + role, 128);
-      const uint32_t (&dk)[4] = tl->dred[role][s][0], (&dv)[4] = tl->dred[role][s][1];
-      const int ke = min(max(int(max(max(dk[0], dk[1]), max(dk[2], dk[3])) >> 23), 27), 227);
-      const int ve = min(max(int(max(max(dv[0], dv[1]), max(dv[2], dv[3])) >> 23), 27), 227);
-      if (role == 0 && t == 0) {
-        const uint32_t (&o)[4] = tl->ok[n & 3];
-        tl->info[n & 3] = uint32_t(ke) | (uint32_t(ve) << 8) | ((o[0] & o[1] & o[2] & o[3]) == 0xffffffffu ? 1u << 16 : 0u);
-      }
-      const float up = pow2_clamped(134 - (role ? ve : ke));  // largest scale to [2^7, 2^8)
-      uint32_t sc[NG];  // rounded to f16: 11 bits
-#pragma unroll
-      for (int q = 0; q < NG; ++q) sc[q] = cvt_f16x2(own[q] * up, own[q] * up);
-      uint8_t* dst = mat + s * kPtMat;
+      wait(&empty[st], ((n / kPtStages) & 1) ^ 1u);
+      uint8_t* dst = mat + st * kPtKv;
 #pragma unroll 1
-      for (int c4 = 0; c4 < 4; ++c4) {  // 32 columns: the front pieces of cur, which then moves up
-        const uint32_t sq = NG == 2 && c4 >= 2 ? sc[NG - 1] : sc[0];
+      for (int c4 = 0; c4 < 2; ++c4) {  // 32 columns: the front pieces of cur, which then moves up
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t p[4];
@@ -770,27 +729,89 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             p[3] = f16x2_sub(((w1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
           }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sq);
-          *reinterpret_cast<uint4*>(dst + (offs[x] ^ ((c4 & 1) << 6))) = make_uint4(p[0], p[1], p[2], p[3]);
+          for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sc[0]);
+          *reinterpret_cast<uint4*>(dst + (sw ^ uint32_t((4 * c4 + x) << 4))) = make_uint4(p[0], p[1], p[2], p[3]);
         }
-        constexpr int STEP = NV / 4;
 #pragma unroll
-        for (int x = 0; x + STEP < NV; ++x) cur[x] = cur[x + STEP];
-        if constexpr (NG == 4) {
-          sc[0] = sc[1];
-          sc[1] = sc[2];
-          sc[2] = sc[3];
-        }
-        if (c4 == 1) dst += kPtHalf;
+        for (int x = 0; x < NV / 2; ++x) cur[x] = cur[x + NV / 2];
+        sc[0] = sc[NS - 1];
       }
-      load();
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
+      if (lane == 0) {
+        mbar_arrive(&full[st]);
+        mbar_arrive(&tl->plan_empty[n % kPtPlans]);
+      }
+      if (n + 1 < total) load(n + 1);
     }
   } else {
     regs_dec<kPtRegsMma>();
-    if (warp < 18) {
+    if (warp >= 18) {
+      // ============================================================= plan
+      // Two warps, every other tile each: where the tile's rows are, their
+      // scales, the largest one's exponent.  Two keys per lane.
+      bool dead = false;
+      PtIter& it = tl->it[warp];
+      int i = it.i0;
+      const uint32_t total = uint32_t(pc.end - pc.at);
+#pragma unroll 1
+      for (uint32_t n = 0; n < total; ++n) {
+        if (int(n & 1) == warp - 18) {
+          const uint32_t sl = n % kPtPlans;
+          const int t0 = it.key0(i) + lane;
+          uint32_t row[2];
+          float sc[2][2][NG], top[2] = {0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int pos = t0 + 32 * x;
+            int page = -1;
+            if (pos < it.tl.kv_end) page = __ldg(a.table + int64_t(it.b) * a.max_pages + (pos >> a.page_log2));
+            // (the rows of one tensor on one GPU are fewer than 2^32)
+            row[x] = unsigned(page) < unsigned(a.n_pages)
+                         ? uint32_t(((int64_t(page) * a.nkv + it.h) << a.page_log2) + (pos & ((1 << a.page_log2) - 1)))
+                         : ~0u;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+              sc[0][x][q] = row[x] != ~0u ? clean_scale(__ldg(a.k_scales + int64_t(row[x]) * NG + q)) : 0.f;
+              sc[1][x][q] = row[x] != ~0u ? clean_scale(__ldg(a.v_scales + int64_t(row[x]) * NG + q)) : 0.f;
+              top[0] = fmaxf(top[0], sc[0][x][q]);
+              top[1] = fmaxf(top[1], sc[1][x][q]);
+            }
+          int e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), 227);
+          const uint32_t ok0 = __ballot_sync(0xffffffffu, row[0] != ~0u), ok1 = __ballot_sync(0xffffffffu, row[1] != ~0u);
+          if (!pt_wait(&tl->plan_empty[sl], ((n / kPtPlans) & 1) ^ 1u, abort)) {
+            if (!dead) tc_give_up(&tl->abort, fault);
+            dead = true;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            tl->row[sl][lane + 32 * x] = row[x];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float up = pow2_clamped(134 - e[y]);  // the largest scale to [2^7, 2^8)
+#pragma unroll
+              for (int q = 0; q < NG; ++q) tl->scale[sl][y][q][lane + 32 * x] = cvt_f16x2(sc[y][x][q] * up, sc[y][x][q] * up);
+            }
+          }
+          if (lane == 0) {
+            tl->ok[n % kPtInfos][0] = ok0;
+            tl->ok[n % kPtInfos][1] = ok1;
+            tl->info[n % kPtInfos] = uint32_t(e[0]) | (uint32_t(e[1]) << 8) | ((ok0 & ok1) == ~0u ? 1u << 16 : 0u);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tl->plan_full[sl]);
+        }
+        if (++i == it.i1) {
+          (void)it.warp_next(a, per);
+          i = it.i0;
+        }
+      }
+    } else {
     // ================================================================== MMAs
     // One warp per group: the control code between the issues takes as long as
     // the products (one warp for both was busy 4500 of 5400 cycles a tile).
@@ -804,66 +825,66 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         on = 0;
       }
     };
-    const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtHalf);
+    const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtKvHalf);
     PtIter& it = tl->it[warp];
     const int m = warp - 16;
     const uint32_t qm = qd + uint32_t(m) * (kPtMat >> 4), sm = uint32_t(128 * m), om = uint32_t(256 + 128 * m);
-    uint32_t n = 0, pu = 0, pp = 0;  // tiles of the CTA; parities of the group's units and tiles
+    uint32_t n = 0, ns = 0, pu = 0;  // tiles of the CTA and of the group; parity of the group's units
+    auto stage = [](uint32_t t) { return t & (kPtStages - 1); };
+    auto phase = [](uint32_t t) { return (t / kPtStages) & 1; };
     do {
       const bool active = it.ntok * a.g > 128 * m;
-      const int halves = 2 * (it.i1 - it.i0);
+      const int tiles = it.i1 - it.i0;
       if (!active) {  // the stages pass unused
 #pragma unroll 1
-        for (int i = 0; i < halves; i += 2, ++n) {
-          wait(&tl->k_full[n & 1], (n >> 1) & 1);
-          pt_arrive(&tl->k_empty[n & 1], on);
-          wait(&tl->v_full[n & 1], (n >> 1) & 1);
-          pt_arrive(&tl->v_empty[n & 1], on);
+        for (int i = 0; i < tiles; ++i, ++n) {
+          wait(&tl->k_full[stage(n)], phase(n));
+          pt_arrive(&tl->k_empty[stage(n)], on);
+          wait(&tl->v_full[stage(n)], phase(n));
+          pt_arrive(&tl->v_empty[stage(n)], on);
         }
         continue;
       }
-      // Step j: O += P V of half j, then S of half j + 2 in P's place.
+      // Step j: O += P V of tile j, then S of tile j + 2 in P's place.
 #pragma unroll 1
-      for (int j = -2; j < halves; ++j) {
-        const uint32_t h = j & 1;
-        const uint32_t vt = n + uint32_t((j >> 1)), kt = vt + 1;  // tiles of the two halves
+      for (int j = -2; j < tiles; ++j) {
+        const uint32_t h = (ns + uint32_t(j)) & 1;  // S buffer of both tiles
+        const uint32_t vt = n + uint32_t(j), kt = vt + 2;
         if (j >= 0) {
-          if (h == 0) wait(&tl->v_full[vt & 1], (vt >> 1) & 1);
+          wait(&tl->v_full[stage(vt)], phase(vt));
           if (j == 0) wait(&tl->o_empty[m], pu ^ 1u);
-          wait(&tl->p_full[m][h], pp);
-          pp ^= h;
+          wait(&tl->p_full[m][h], ((ns + uint32_t(j)) >> 1) & 1);
           tc_fence_after();
-          const uint32_t av = sm + 64 * h + 32, bv = vd + (vt & 1) * (kPtMat >> 4) + h * (8192 >> 4);
+          const uint32_t av = sm + 64 * h + 32, bv = vd + stage(vt) * (kPtKv >> 4);
 #pragma unroll
           for (uint32_t k = 0; k < 4; ++k) pt_mma_ts(om, av + 8 * k, bv + k * (2048 >> 4), kPtIdescPV, k > 0 ? 1u : uint32_t(j > 0), on);
           pt_commit(&tl->pv_done[m], on);
-          if (h) pt_commit(&tl->v_empty[vt & 1], on);
+          pt_commit(&tl->v_empty[stage(vt)], on);
         }
-        if (j + 2 < halves) {
+        if (j + 2 < tiles) {
           if (j == -2) wait(&tl->q_full[m], pu);
-          if (h == 0) wait(&tl->k_full[kt & 1], (kt >> 1) & 1);
+          wait(&tl->k_full[stage(kt)], phase(kt));
           tc_fence_after();
-          const uint32_t bk = kd + (kt & 1) * (kPtMat >> 4) + h * (8192 >> 4);
+          const uint32_t bk = kd + stage(kt) * (kPtKv >> 4);
 #pragma unroll
-          for (uint32_t k = 0; k < 8; ++k) {
-            const uint32_t o = ((k >> 2) * kPtHalf + (k & 3) * 32) >> 4;
-            pt_mma_ss(sm + 64 * h, qm + o, bk + o, kPtIdescQK, k > 0, on);
-          }
+          for (uint32_t k = 0; k < 8; ++k)
+            pt_mma_ss(sm + 64 * h, qm + (((k >> 2) * kPtHalf + (k & 3) * 32) >> 4), bk + (((k >> 2) * kPtKvHalf + (k & 3) * 32) >> 4), kPtIdescQK, k > 0, on);
           // The softmax reads what the key warps wrote beside the keys
           // (exponents, cached bits) once S is there: this warp has seen their
           // arrival and passes it on.  (They cannot wait for k_full
           // themselves: it may be a phase further on by then.)
           pt_arrive(&tl->s_full[m][h], on);
           pt_commit(&tl->s_full[m][h], on);
-          if (h) pt_commit(&tl->k_empty[kt & 1], on);
+          pt_commit(&tl->k_empty[stage(kt)], on);
         }
       }
       pt_commit(&tl->o_full[m], on);
-      n += uint32_t(halves) / 2;
+      n += uint32_t(tiles);
+      ns += uint32_t(tiles);
       pu ^= 1;
     } while (it.warp_next(a, per));
     // every MMA is complete before TMEM is freed (passes at once normally)
-    if (on) (void)pt_wait(&tl->v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, nullptr);
+    if (on) (void)pt_wait(&tl->v_empty[stage(n - 1)], phase(n - 1), nullptr);
     __syncwarp();
     }
   }
