@@ -10,7 +10,7 @@
 //    the tile's largest scale, so both fill the f16 range from the top
 //    whatever the scales are.  The scale and the product are rounded to
 //    f16: 11 bits, where the output has 8;
-//  * the rotated query is scaled by a bound of its group's largest entry;
+//  * each rotated query is scaled by the exponent of a bound of its entries;
 //  * the exponents come back as one multiplier per tile in the exponent's fma
 //    (scores) and as a summand of the softmax reference (values): with
 //    m >= max(score + e), a weight is 2^(score + e - m) <= 2^8, and l counts
@@ -134,7 +134,7 @@ struct PtTail {
   uint32_t ok[kPtInfos][2];  // the tile's keys that are cached
   uint32_t row[kPtPlans][kPtTile];       // rows of the tile's keys in the pool, ~0: not cached
   uint32_t scale[kPtPlans][2][4][kPtTile];  // K and V scales over 2^e as f16 pairs, by group
-  uint32_t red[2][4];       // group maxima of the rows' sums of |q|
+  int eq[2][128];            // exponents of the groups' rows
   uint32_t sgn[4];          // sign bits of the 128 columns
   int last[2];
   uint32_t tmem_base;
@@ -389,74 +389,102 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         dead = true;
       }
     };
-    int eq = 0;  // the group's queries are scaled by 2^eq
+    int eq = 0;  // this row's query is scaled by 2^eq
     uint32_t n = 0, ns = 0, nu = 0;  // tiles of the CTA, tiles and units of this group
     bool active = false;             // the group has rows in unit `it`
     float M = -INFINITY, l = 0.f;
     PtIter &it = tl->it[warp], &nx = tl->next[warp];
 
-    // Rows of 128 in two halves of 64: the butterfly between the halves as
-    // they are read, then H_64.  The raw row waits in its own place in shared
-    // memory.  The group's exponent comes from the rows' sums of |x|, which no
-    // rotated entry exceeds.
+    // A warp rotates its 32 rows 16 at a time: four of the seven stages as an
+    // exact bf16 product with H_16 (lane (g, j) holds columns 32 j .. + 31 of
+    // rows g and g + 8, as in the append kernel), three in registers.  Each row
+    // is scaled by the exponent of a bound of its entries, 128 times its
+    // largest input.
     auto load_queries = [&](const PtIter& u) {
-      const int row = 128 * m + r;
-      uint8_t* dst = qs + m * kPtMat + r * 128;
-      auto chunk = [&](int c) { return reinterpret_cast<uint4*>(dst + (c >> 3) * kPtHalf + (((c & 7) ^ (r & 7)) << 4)); };
-      float sum = 0.f;
-      const bool live = row < u.ntok * a.g;
-      const int tok = row / a.g, hh = row - tok * a.g;
-      const uint4* p = reinterpret_cast<const uint4*>(a.q + (live ? int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim : 0));
+      const int g = lane >> 2, j = lane & 3;
+      uint32_t bm[2][2];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        uint4 w = live ? __ldg(p + c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t sg = tl->sgn[c >> 2] >> (8 * (c & 3));  // signs of the eight columns
-        auto flip = [&](uint32_t x, int k) { return x ^ (((sg >> (2 * k)) & 1u) << 15) ^ (((sg >> (2 * k + 1)) & 1u) << 31); };
-        w = make_uint4(flip(w.x, 0), flip(w.y, 1), flip(w.z, 2), flip(w.w, 3));
-        sum += fabsf(bf16lo(w.x)) + fabsf(bf16hi(w.x)) + fabsf(bf16lo(w.y)) + fabsf(bf16hi(w.y)) + fabsf(bf16lo(w.z)) + fabsf(bf16hi(w.z)) +
-               fabsf(bf16lo(w.w)) + fabsf(bf16hi(w.w));
-        *chunk(c) = w;
-      }
-      const uint32_t wt = __reduce_max_sync(0xffffffffu, __float_as_uint(sum * a.qmul));
-      if (lane == 0) tl->red[m][warp & 3] = wt;
-      named_bar_sync(1 + m, 128);
-      const uint32_t gt = max(max(tl->red[m][0], tl->red[m][1]), max(tl->red[m][2], tl->red[m][3]));
-      // the bound to [2^14, 2^15); a group whose entries are all below 2^-100
-      // counts as zero
-      const int ge = min(int(gt >> 23), 253);
-      const bool zero = ge < 27;
-      eq = zero ? 0 : 141 - ge;
-      const float up = zero ? 0.f : a.qmul * pow2_clamped(eq);
-      auto half = [&](bool upper, uint32_t (&out)[32]) {
-        float y[64];
+      for (int c = 0; c < 2; ++c) h16_operand(g, j, c, 0x3F80u, bm[c]);
+      const uint32_t sg = tl->sgn[j];
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        const int r0 = 32 * (warp & 3) + 16 * pass + g;  // rows r0, r0 + 8 of the group
+        uint4 in[2][4];
+        float up[2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = *chunk(c), w = *chunk(c + 8);
-          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+        for (int x = 0; x < 2; ++x) {
+          const int row = 128 * m + r0 + 8 * x;
+          const int tok = row / a.g, hh = row - tok * a.g;
+          const bool live = row < u.ntok * a.g;
+          const uint4* p = reinterpret_cast<const uint4*>(
+              a.q + (live ? int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim + 32 * j : 0));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) in[x][i] = live ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t top = 0;  // largest magnitudes of the even and the odd columns, as bf16 bits
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            top = __vmaxu2(top, in[x][i].x & 0x7FFF7FFFu);
+            top = __vmaxu2(top, in[x][i].y & 0x7FFF7FFFu);
+            top = __vmaxu2(top, in[x][i].z & 0x7FFF7FFFu);
+            top = __vmaxu2(top, in[x][i].w & 0x7FFF7FFFu);
+          }
+          uint32_t mx = max(top & 0xFFFFu, top >> 16);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // the bound to [2^14, 2^15); a row whose entries are all below 2^-100
+          // counts as zero
+          const float bound = __uint_as_float(mx << 16) * 128.f * a.qmul;
+          const int be = min(int(__float_as_uint(bound) >> 23), 253);
+          const int e = be < 27 ? 0 : 141 - be;
+          up[x] = be < 27 ? 0.f : a.qmul * pow2_clamped(e);
+          if (j == 0) tl->eq[m][r0 + 8 * x] = e;
+        }
+        float v[2][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[2][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[8 * c + 2 * k] = upper ? bf16lo(vv[k]) - bf16lo(ww[k]) : bf16lo(vv[k]) + bf16lo(ww[k]);
-            y[8 * c + 2 * k + 1] = upper ? bf16hi(vv[k]) - bf16hi(ww[k]) : bf16hi(vv[k]) + bf16hi(ww[k]);
+            const uint32_t flip = (((sg >> (8 * i + 2 * k)) & 1u) << 15) | (((sg >> (8 * i + 2 * k + 1)) & 1u) << 31);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) w[x][k] = (k == 0 ? in[x][i].x : k == 1 ? in[x][i].y : k == 2 ? in[x][i].z : in[x][i].w) ^ flip;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_h16_bf16(d, w[0][2 * h], w[1][2 * h], w[0][2 * h + 1], w[1][2 * h + 1], bm[c][0], bm[c][1]);
+              v[0][8 * i + 4 * h + 2 * c] = d[0];
+              v[0][8 * i + 4 * h + 2 * c + 1] = d[1];
+              v[1][8 * i + 4 * h + 2 * c] = d[2];
+              v[1][8 * i + 4 * h + 2 * c + 1] = d[3];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          reg_stage<32, 4>(v[x]);
+          reg_stage<32, 8>(v[x]);
+          reg_stage<32, 16>(v[x]);
+          const int r = r0 + 8 * x;
+          uint8_t* dst = qs + m * kPtMat + (j >> 1) * kPtHalf + r * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = cvt_f16x2(v[x][8 * i + pt_column<BITS>(2 * k)] * up[x], v[x][8 * i + pt_column<BITS>(2 * k + 1)] * up[x]);
+            *reinterpret_cast<uint4*>(dst + (((4 * (j & 1) + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        reg_fwht<64, 6>(y);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int c = 8 * (k >> 2), q = 2 * (k & 3);
-          out[k] = cvt_f16x2(y[c + pt_column<BITS>(q)] * up, y[c + pt_column<BITS>(q + 1)] * up);
-        }
-      };
-      uint32_t o0[32], o1[32];
-      half(false, o0);
-      half(true, o1);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        *chunk(c) = make_uint4(o0[4 * c], o0[4 * c + 1], o0[4 * c + 2], o0[4 * c + 3]);
-        *chunk(c + 8) = make_uint4(o1[4 * c], o1[4 * c + 1], o1[4 * c + 2], o1[4 * c + 3]);
       }
       fence_async_shared();
-      named_bar_sync(1 + m, 128);  // tl->red has been read; the group's rows are written
+      named_bar_sync(1 + m, 128);  // the group's rows are written
       if (lane == 0) mbar_arrive(&tl->q_full[m]);
+      eq = tl->eq[m][r];
     };
 
     // The unit's partial O to the workspace; the last CTA to come sums them up
