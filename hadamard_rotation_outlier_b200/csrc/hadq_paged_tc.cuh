@@ -135,7 +135,7 @@ struct PtTail {
   uint32_t row[kPtPlans][kPtTile];       // rows of the tile's keys in the pool, ~0: not cached
   uint32_t scale[kPtPlans][2][4][kPtTile];  // K and V scales over 2^e as f16 pairs, by group
   int eq[2][128];            // exponents of the groups' rows
-  uint32_t sgn[4];          // sign bits of the 128 columns
+  alignas(16) uint32_t flip[64];  // the signs of the 128 columns as masks of bf16 pairs
   int last[2];
   uint32_t tmem_base;
   uint32_t abort;
@@ -339,10 +339,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     tl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp < 4) {
-    const uint32_t bits = __ballot_sync(0xffffffffu, a.signs && a.signs[tid] < 0);
-    if (lane == 0) tl->sgn[warp] = bits;
-  }
+  if (tid < 64) tl->flip[tid] = a.signs ? pair_sign_mask(a.signs[2 * tid], a.signs[2 * tid + 1]) : 0u;
   if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tl->tmem_base)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -405,7 +402,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       uint32_t bm[2][2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) h16_operand(g, j, c, 0x3F80u, bm[c]);
-      const uint32_t sg = tl->sgn[j];
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         const int r0 = 32 * (warp & 3) + 16 * pass + g;  // rows r0, r0 + 8 of the group
@@ -446,11 +442,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t w[2][4];
+          const uint4 flip = *reinterpret_cast<const uint4*>(&tl->flip[16 * j + 4 * i]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t flip = (((sg >> (8 * i + 2 * k)) & 1u) << 15) | (((sg >> (8 * i + 2 * k + 1)) & 1u) << 31);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) w[x][k] = (k == 0 ? in[x][i].x : k == 1 ? in[x][i].y : k == 2 ? in[x][i].z : in[x][i].w) ^ flip;
+            for (int x = 0; x < 2; ++x)
+              w[x][k] = (k == 0 ? in[x][i].x ^ flip.x : k == 1 ? in[x][i].y ^ flip.y : k == 2 ? in[x][i].z ^ flip.z : in[x][i].w ^ flip.w);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -469,6 +466,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           reg_stage<32, 4>(v[x]);
           reg_stage<32, 8>(v[x]);
           reg_stage<32, 16>(v[x]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) mul2(v[x][i], v[x][i + 1], up[x]);
           const int r = r0 + 8 * x;
           uint8_t* dst = qs + m * kPtMat + (j >> 1) * kPtHalf + r * 128;
 #pragma unroll
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = cvt_f16x2(v[x][8 * i + pt_column<BITS>(2 * k)] * up[x], v[x][8 * i + pt_column<BITS>(2 * k + 1)] * up[x]);
+              w[k] = cvt_f16x2(v[x][8 * i + pt_column<BITS>(2 * k)], v[x][8 * i + pt_column<BITS>(2 * k + 1)]);
             *reinterpret_cast<uint4*>(dst + (((4 * (j & 1) + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -563,20 +562,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           float w[32];
           tmem_ld32(tO + 32 * q, *reinterpret_cast<float(*)[32]>(y + 32 * q));
           tmem_ld32(tO + 64 + 32 * q, w);
+          const float sg = h ? -1.f : 1.f;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) y[32 * q + k] = h ? y[32 * q + k] - w[k] : y[32 * q + k] + w[k];
+          for (int k = 0; k < 32; ++k) y[32 * q + k] = fmaf(w[k], sg, y[32 * q + k]);
         }
         reg_fwht<64, 6>(y);
         if (store) {
-          const uint32_t sg[2] = {tl->sgn[2 * h], tl->sgn[2 * h + 1]};
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) mul2(y[k], y[k + 1], inv);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = cvt_bf16x2(y[8 * c + pt_position<BITS>(2 * k)] * inv, y[8 * c + pt_position<BITS>(2 * k + 1)] * inv) ^
-                     (((sg[c >> 2] >> (8 * (c & 3) + 2 * k)) & 1u) << 15) ^ (((sg[c >> 2] >> (8 * (c & 3) + 2 * k + 1)) & 1u) << 31);
-            dst[8 * h + c] = make_uint4(w[0], w[1], w[2], w[3]);
+            const uint4 flip = *reinterpret_cast<const uint4*>(&tl->flip[32 * h + 4 * c]);
+            const float* z = y + 8 * c;
+            dst[8 * h + c] = make_uint4(cvt_bf16x2(z[pt_position<BITS>(0)], z[pt_position<BITS>(1)]) ^ flip.x,
+                                        cvt_bf16x2(z[pt_position<BITS>(2)], z[pt_position<BITS>(3)]) ^ flip.y,
+                                        cvt_bf16x2(z[pt_position<BITS>(4)], z[pt_position<BITS>(5)]) ^ flip.z,
+                                        cvt_bf16x2(z[pt_position<BITS>(6)], z[pt_position<BITS>(7)]) ^ flip.w);
           }
         }
       }
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       if (!more) break;
       __syncwarp();
       if (lane == 0) it = nx;
-      __syncwarp();
+      more = nx.warp_next(a, per);  // (looked up while this unit runs)
       active = next_active;
       M = -INFINITY;
       l = 0.f;
@@ -694,7 +695,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       } else {
         n += it.i1 - it.i0;
       }
-      more = nx.warp_next(a, per);
     }
   } else if (warp < 16) {
     // ======================================================= keys and values
