@@ -166,36 +166,45 @@ __device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPl
 // ------------------------------------------------------- few query rows
 //
 // One pass over a unit's keys for 8 * RG query rows (RG = 1 or 2).  A warp
-// takes 16 keys at a time through its own cp.async ring:
+// takes 32 keys at a time through its own cp.async ring:
 //  * scores by m16n8k32 s8 products: A = the query cut into two signed 8-bit
 //    digits of a 16-bit fixed-point number (row r: high digits, row r + 8: low
 //    digits), B = the key codes.  The integer sums are exact, and a lane's
 //    accumulators hold both digits of one row against its own keys;
 //  * the weights as a transposed product O^T += V^T P^T, m16n8k16 f16: A =
-//    value codes, exact in f16 (times the ratio of a group's scale to the
-//    row's largest, for groups below 128), B = the weights, which the lane
-//    already holds where this operand wants them.  No shuffle but the two of
-//    the row maximum.
-// A weight enters as f16 times its value row's scale over 2^e, e the exponent
-// of the largest value scale among the 16 keys, and the running reference
-// counts e in: m = max(score + e), so an f16 weight is at most 2^9 whatever
-// the scales are (11 bits kept, against the 8 of the bf16 output); l and O are
-// float32.
+//    value codes, exact in f16, B = the weights times the keys' value scales
+//    (one such operand per scale group, and the 16 value columns of an MMA lie
+//    in one group), which the lane already holds where this operand wants
+//    them.  No shuffle but the two of the row maximum.
+// A weight enters as f16 times its value scale over 2^e, e the exponent of the
+// largest value scale among the 32 keys, and the running reference counts e
+// in: m = max(score + e), so an f16 weight is at most 2^9 whatever the scales
+// are (11 bits kept, against the 8 of the bf16 output); l and O are float32.
 //
-// Bound by HBM for long INT8 caches and close to the issue rate for INT4: a
-// cached row pair is 2 * (16 BITS + 512 / G) bytes against about 11 warp
-// instructions.
+// Bound by HBM for long INT8 caches and by the issue rate for INT4: a cached
+// row pair is 2 * (16 BITS + 512 / G) bytes against about 13 warp
+// instructions, most of them for the value codes.
 constexpr int kPdThreads = 128;
 constexpr int kPdWarps = 4;
-constexpr int kPdTile = 64;  // keys per CTA step, 16 per warp
+constexpr int kPdStep = 32;                     // keys per warp and step
+constexpr int kPdTile = kPdWarps * kPdStep;     // keys per CTA and step
 constexpr int kPdPitch = kPagedDim + 4;
 
-__host__ __device__ constexpr int pd_stages(int bits) { return bits == 8 ? 3 : 4; }
+__host__ __device__ constexpr int pd_stages(int bits) { return bits == 8 ? 2 : 3; }
+// A stage: 32 K rows, 32 V rows (pitches as in the contiguous kernel), then
+// [32][NG] K scales and as many V scales.
+template <int NG, int BITS>
+struct PdStage {
+  using RW = AttnRows<BITS>;
+  static constexpr int V = kPdStep * RW::KP;
+  static constexpr int S = V + kPdStep * RW::VROW;
+  static constexpr int BYTES = S + 2 * kPdStep * 4 * NG;
+};
 
 template <int RG, int NG, int BITS>
 struct __align__(16) PdSmem {
   union {
-    uint8_t stage[kPdWarps][pd_stages(BITS)][attn_stage_bytes(NG, BITS)];
+    uint8_t stage[kPdWarps][pd_stages(BITS)][PdStage<NG, BITS>::BYTES];
     float comb[kPdWarps][8 * RG][kPdPitch];
   } u;
   int8_t qd[2][8 * RG][kPagedDim];  // query digits: high, low
@@ -204,6 +213,13 @@ struct __align__(16) PdSmem {
   PagedPlanSmem plan;
   int last;
 };
+
+// The first of a chain of s8 products: D = A B.
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+}
 
 // 4 nibbles of two tokens (a: low half, b: high half of x) -> f16 pairs.
 __device__ __forceinline__ void i4x4_to_f16_tokens(uint32_t x, uint32_t (&r)[4]) {
@@ -244,15 +260,27 @@ __device__ __forceinline__ void warp_h128(float (&y)[4], int lane) {
   }
 }
 
+// The order in which a row's 128 values are kept: a lane's 16 value columns
+// are D = 16 / NG consecutive ones of every scale group, column (128 / NG) q +
+// D g + e at idx = 8 (D q + e) + g, a permutation of index bits, under which
+// H_128 is unchanged.
+template <int NG>
+__device__ __forceinline__ int pd_column(int idx) {
+  constexpr int D = 16 / NG;
+  const int qe = idx >> 3, g = idx & 7;
+  return (128 / NG) * (qe / D) + D * g + qe % D;
+}
+
 // One finished output row: rotate back, normalise, sign, store.  The lane's
-// y[r] is index 4 * lane + r of the order idx = 8 (dim & 15) + (dim >> 4).
+// y[r] is index 4 * lane + r.
+template <int NG>
 __device__ __forceinline__ void pd_finish(const PagedAttnArgs& a, float4 acc, float L, uint16_t* row, int lane) {
   float y[4] = {acc.x, acc.y, acc.z, acc.w};
   warp_h128(y, lane);
   const float inv = L > 0.f ? a.inv_sqrt_dim / L : 0.f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const int dim = 64 * (lane & 1) + 16 * r + (lane >> 1);
+    const int dim = pd_column<NG>(4 * lane + r);
     float v = y[r] * inv;
     if (a.signs && a.signs[dim] < 0) v = -v;
     row[dim] = uint16_t(pack_bf16x2(v, 0.f));
@@ -260,10 +288,10 @@ __device__ __forceinline__ void pd_finish(const PagedAttnArgs& a, float4 acc, fl
 }
 
 template <int RG, int NG, int BITS>
-__global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kernel(const PagedAttnArgs a) {
   using RW = AttnRows<BITS>;
-  constexpr int KROW = RW::KROW, KP = RW::KP, VROW = RW::VROW, STV = RW::STV, STS = RW::STS;
-  constexpr int SB = attn_stage_bytes(NG, BITS);
+  using ST = PdStage<NG, BITS>;
+  constexpr int KROW = RW::KROW, KP = RW::KP, VROW = RW::VROW;
   constexpr int STAGES = pd_stages(BITS);
   constexpr int ROWS = 8 * RG;
   extern __shared__ __align__(16) uint8_t pd_smem_raw[];
@@ -349,7 +377,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
       }
       *reinterpret_cast<uint32_t*>(&sm.qd[0][r][4 * lane]) = hi;
       *reinterpret_cast<uint32_t*>(&sm.qd[1][r][4 * lane]) = lo;
-      if (lane == 0) sm.qscale[r] = zero ? 0.f : amax * (BITS == 4 ? 1.f / (16.f * 32000.f) : 1.f / 32000.f);
+      // (positive even then: it multiplies the -inf of unseen keys)
+      if (lane == 0) sm.qscale[r] = zero ? 1.f : amax * (BITS == 4 ? 1.f / (16.f * 32000.f) : 1.f / 32000.f);
     }
     __syncthreads();
 
@@ -380,43 +409,56 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
     const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
 
     // ---- this warp's ring ----
-    auto key0 = [&](int k) {  // first of this warp's 16 keys in step k
+    auto key0 = [&](int k) {  // first of this warp's 32 keys in step k
       const int i = i0 + k;
-      return (i < tl.head ? i : i - tl.head + tl.from) * kPdTile + 16 * w;
+      return (i < tl.head ? i : i - tl.head + tl.from) * kPdTile + kPdStep * w;
     };
     const int32_t* tab = a.table + int64_t(b) * a.max_pages;
-    auto page_of = [&](int k) {  // page of step k's keys, -1: none of them is cached
-      if (k >= nw) return -1;
+    // Pages of step k's two runs of 16 keys, -1: none of them is cached.
+    auto pages_of = [&](int k, int (&pg)[2]) {
+      pg[0] = pg[1] = -1;
+      if (k >= nw) return;
       const int t = key0(k);
-      if (t >= tl.kv_end) return -1;
-      const int p = __ldg(tab + (t >> a.page_log2));
-      return unsigned(p) < unsigned(a.n_pages) ? p : -1;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (t + 16 * x < tl.kv_end) pg[x] = __ldg(tab + ((t + 16 * x) >> a.page_log2));
     };
-    constexpr int CPR = KROW / 16, TPP = 32 / CPR, NPASS = 16 / TPP;
+    // Copies: a lane takes piece lane % CPR of rows lane / CPR + TPP p, p =
+    // 0 .. NP - 1 for each run of 16 keys.
+    constexpr int CPR = KROW / 16, TPP = 32 / CPR, NP = 16 / TPP;
     const int ctok = lane / CPR, cpart = lane % CPR;
     const uint32_t s_ring = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.u.stage[w][0][0]));
-    const uint32_t d_k = ctok * KP + cpart * 16, d_v = STV + ctok * VROW + cpart * 16;
-    const int src0 = ctok * KROW + cpart * 16;
-    uint32_t okbits = 0;  // bit (step % 8): the step's keys are in the ring
-    auto issue = [&](int k, int page) {
-      okbits &= ~(1u << (k & 7));
-      if (page >= 0) {
-        okbits |= 1u << (k & 7);
-        const int64_t row = ((int64_t(page) * a.nkv + h) << a.page_log2) + (key0(k) & ((1 << a.page_log2) - 1));
-        const uint32_t st = s_ring + uint32_t(k % STAGES) * SB;
-        const uint8_t* gk = a.k_codes + row * KROW + src0;
-        const uint8_t* gv = a.v_codes + row * KROW + src0;
+    const uint32_t d_k = ctok * KP + cpart * 16, d_v = ST::V + ctok * VROW + cpart * 16;
+    const uint8_t* gk0 = a.k_codes + ctok * KROW + cpart * 16;
+    const uint8_t* gv0 = a.v_codes + ctok * KROW + cpart * 16;
+    // Scales: 4 NG pieces of 16 bytes for each run and tensor; lanes below
+    // 4 NG take the K scales, the next 4 NG the V scales.
+    const float* gs0 = (lane < 4 * NG ? a.k_scales : a.v_scales) + 4 * (lane % (4 * NG));
+    const uint32_t d_s = ST::S + (lane < 4 * NG ? 0 : kPdStep * 4 * NG) + 16 * (lane % (4 * NG));
+    uint32_t okbits = 0;  // bits 2 (step % STAGES), + 1: the step's runs are in the ring
+    int slot_in = 0;      // ring slot of the next step to load
+    auto issue = [&](int k, const int (&pg)[2]) {
+      const uint32_t st = s_ring + uint32_t(slot_in) * ST::BYTES;
+      okbits &= ~(3u << (2 * slot_in));
+      const int off = key0(k) & ((1 << a.page_log2) - 1);
 #pragma unroll
-        for (int p = 0; p < NPASS; ++p) {
-          cp_async16(st + d_k + TPP * p * KP, gk + TPP * p * KROW);
-          cp_async16(st + d_v + TPP * p * VROW, gv + TPP * p * KROW);
-        }
-        if (lane < 8 * NG) {  // 4 NG pieces of 16 bytes of K scales, then as many of V
-          const float* gs = (lane < 4 * NG ? a.k_scales : a.v_scales) + row * NG + 4 * (lane % (4 * NG));
-          cp_async16(st + STS + 16 * lane, gs);
+      for (int x = 0; x < 2; ++x) {
+        if (unsigned(pg[x]) < unsigned(a.n_pages)) {
+          okbits |= 1u << (2 * slot_in + x);
+          // (the rows of one tensor on one GPU are fewer than 2^32)
+          const uint32_t row = ((uint32_t(pg[x]) * uint32_t(a.nkv) + uint32_t(h)) << a.page_log2) +
+                               ((off + 16 * x) & ((1 << a.page_log2) - 1));
+          const uint64_t at = uint64_t(row) * KROW;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            cp_async16(st + d_k + (16 * x + TPP * p) * KP, gk0 + at + TPP * p * KROW);
+            cp_async16(st + d_v + (16 * x + TPP * p) * VROW, gv0 + at + TPP * p * KROW);
+          }
+          if (lane < 8 * NG) cp_async16(st + d_s + 16 * x * 4 * NG, gs0 + uint64_t(row) * NG);
         }
       }
       cp_async_commit();
+      slot_in = slot_in + 1 == STAGES ? 0 : slot_in + 1;
     };
 
     float o[RG][8][4];
@@ -429,66 +471,87 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
       l_run[k] = 0.f;
     }
     {
-      int pg[STAGES - 1];
+      int pg[STAGES - 1][2];
 #pragma unroll
-      for (int k = 0; k < STAGES - 1; ++k) pg[k] = page_of(k);
+      for (int k = 0; k < STAGES - 1; ++k) pages_of(k, pg[k]);
 #pragma unroll
-      for (int k = 0; k < STAGES - 1; ++k) issue(k, pg[k]);
+      for (int k = 0; k < STAGES - 1; ++k) {
+        if (k < nw) {
+          issue(k, pg[k]);
+        } else {
+          cp_async_commit();
+          slot_in = slot_in + 1 == STAGES ? 0 : slot_in + 1;
+        }
+      }
     }
-    int pg_next = page_of(STAGES - 1);
+    int pg_next[2];
+    pages_of(STAGES - 1, pg_next);
+    int slot_out = 0;
 
     for (int k = 0; k < nw; ++k) {
-      issue(k + STAGES - 1, pg_next);
-      pg_next = page_of(k + STAGES);
+      if (k + STAGES - 1 < nw) {
+        issue(k + STAGES - 1, pg_next);
+        pages_of(k + STAGES, pg_next);
+      } else {
+        cp_async_commit();
+      }
       cp_async_wait<STAGES - 1>();
       __syncwarp();
-      if ((okbits >> (k & 7)) & 1u) {
-        const uint8_t* st = sm.u.stage[w][k % STAGES];
-        const float* sc = reinterpret_cast<const float*>(st + STS);  // [16][NG] K, then [16][NG] V
+      const uint32_t ok = (okbits >> (2 * slot_out)) & 3u;
+      uint8_t* st = sm.u.stage[w][slot_out];
+      slot_out = slot_out + 1 == STAGES ? 0 : slot_out + 1;
+      if (ok) {
+        const float* ksc = reinterpret_cast<const float*>(st + ST::S);  // [32][NG]
+        float* vsc = reinterpret_cast<float*>(st + ST::S) + kPdStep * NG;
         const int t0 = key0(k);
 
-        // exponent of the largest value scale among the 16 keys
-        float vmax = 0.f;
+        // Value scales over 2^e, in place, a key per lane; a key that is not
+        // there has none.
+        int ve;
+        {
+          const bool there = t0 + lane < tl.kv_end && ((ok >> (lane >> 4)) & 1u);
+          float v[NG], top = 0.f;
 #pragma unroll
-        for (int q = 0; q < (NG + 1) / 2; ++q) vmax = fmaxf(vmax, clean_scale(sc[16 * NG + 32 * q + (NG == 1 ? lane & 15 : lane)]));
-        const int ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)) >> 23), 27), 227);
+          for (int q = 0; q < NG; ++q) {
+            v[q] = there ? clean_scale(vsc[lane * NG + q]) : 0.f;
+            top = fmaxf(top, v[q]);
+          }
+          ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), 27), 227);
+          const float down = __uint_as_float(uint32_t(254 - ve) << 23);
+#pragma unroll
+          for (int q = 0; q < NG; ++q) vsc[lane * NG + q] = v[q] * down;
+          __syncwarp();
+        }
         const float vdown = __uint_as_float(uint32_t(254 - ve) << 23);  // 2^-e
         const float vexp = float(ve - 127);                             // e
 
-        // ---- scores of 8 RG rows x 16 keys ----
-        int c[RG][2][NG][4];
+        // ---- scores of 8 RG rows x 32 keys, over the rows' query scales; this
+        // lane's keys are 8 x + 2 j, + 1 ----
+        float s[RG][4][2];
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
-#pragma unroll
-          for (int q = 0; q < NG; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[r][0][q][i] = c[r][1][q][i] = 0;
-        if constexpr (BITS == 4) {
-          uint32_t kw[2][4];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint8_t* kr = st + (g + 8 * x) * KP;
+        for (int x = 0; x < 4; ++x) {
+          const uint8_t* kr = st + (8 * x + g) * KP;
+          int c[RG][NG][4];
+          if constexpr (BITS == 4) {
+            uint32_t kw[4];
             if constexpr (NG == 1) {
               const uint4 v = *reinterpret_cast<const uint4*>(kr + 16 * j);
-              kw[x][0] = v.x; kw[x][1] = v.y; kw[x][2] = v.z; kw[x][3] = v.w;
+              kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
             } else {
 #pragma unroll
-              for (int s = 0; s < 4; ++s) kw[x][s] = *reinterpret_cast<const uint32_t*>(kr + 16 * s + 4 * j);
+              for (int q = 0; q < 4; ++q) kw[q] = *reinterpret_cast<const uint32_t*>(kr + 16 * q + 4 * j);
             }
-          }
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int q = 0; q < 4; ++q) {
               uint32_t e, od;
-              int4x8_to_s8x16(kw[x][s], e, od);
+              int4x8_to_s8x16(kw[q], e, od);
 #pragma unroll
-              for (int r = 0; r < RG; ++r) mma_s8_16832(c[r][x][s * NG / 4], qa[r][s], e, od);
+              for (int r = 0; r < RG; ++r) {
+                if (q % (4 / NG) == 0) mma_s8_first(c[r][q * NG / 4], qa[r][q], e, od);
+                else mma_s8_16832(c[r][q * NG / 4], qa[r][q], e, od);
+              }
             }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint8_t* kr = st + (g + 8 * x) * KP;
+          } else {
             uint2 kw[4];
             if constexpr (NG == 1) {
               const uint4 v0 = *reinterpret_cast<const uint4*>(kr + 32 * j);
@@ -497,66 +560,58 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
               kw[2] = make_uint2(v1.x, v1.y); kw[3] = make_uint2(v1.z, v1.w);
             } else {
 #pragma unroll
-              for (int s = 0; s < 4; ++s) kw[s] = *reinterpret_cast<const uint2*>(kr + 32 * s + 8 * j);
+              for (int q = 0; q < 4; ++q) kw[q] = *reinterpret_cast<const uint2*>(kr + 32 * q + 8 * j);
             }
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const uint32_t e = __byte_perm(kw[s].x, kw[s].y, 0x6420), od = __byte_perm(kw[s].x, kw[s].y, 0x7531);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t e = __byte_perm(kw[q].x, kw[q].y, 0x6420), od = __byte_perm(kw[q].x, kw[q].y, 0x7531);
 #pragma unroll
-              for (int r = 0; r < RG; ++r) mma_s8_16832(c[r][x][s * NG / 4], qa[r][s], e, od);
+              for (int r = 0; r < RG; ++r) {
+                if (q % (4 / NG) == 0) mma_s8_first(c[r][q * NG / 4], qa[r][q], e, od);
+                else mma_s8_16832(c[r][q * NG / 4], qa[r][q], e, od);
+              }
             }
           }
-        }
-
-        // this lane's keys: 2j, 2j + 1 (x = 0) and 2j + 8, 2j + 9 (x = 1)
-        float kscl[2][2][NG];
-        float pvs[2][2];   // value scale (the row's largest) over 2^e
-        float ratio[2][2]; // groups: this lane's group of value dims over the row's largest
+          float ksl[2][NG];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int t = 2 * j + 8 * x + y;
+            for (int q = 0; q < NG; ++q) ksl[y][q] = ksc[(8 * x + 2 * j + y) * NG + q];
 #pragma unroll
-            for (int q = 0; q < NG; ++q) kscl[x][y][q] = sc[t * NG + q];
-            float top = 0.f;
-#pragma unroll
-            for (int q = 0; q < NG; ++q) top = fmaxf(top, clean_scale(sc[(16 + t) * NG + q]));
-            pvs[x][y] = top * vdown;
-            ratio[x][y] = 0.f;
-            if constexpr (NG > 1) ratio[x][y] = top > 0.f ? clean_scale(sc[(16 + t) * NG + (g * NG >> 3)]) / top : 0.f;
-          }
-
-        const bool masked = t0 + 16 > all_lim || (a.window > 0 && t0 < all_low);
-        uint32_t pb[RG][2];
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          float s[2][2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int r = 0; r < RG; ++r)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float v = 0.f;
 #pragma unroll
               for (int q = 0; q < NG; ++q) {
-                const float p = float(c[r][x][q][y] * 256 + c[r][x][q][2 + y]);
-                v = NG == 1 ? p * kscl[x][y][q] : fmaf(p, kscl[x][y][q], v);
+                const float p = float(c[r][q][y] * 256 + c[r][q][2 + y]);
+                v = q == 0 ? p * ksl[y][q] : fmaf(p, ksl[y][q], v);
               }
-              s[x][y] = v * qs[r];
+              s[r][x][y] = v;
             }
+        }
+
+        const bool masked = ok != 3u || t0 + kPdStep > all_lim || (a.window > 0 && t0 < all_low);
+        float p[RG][4][2];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
           if (masked) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const int t = t0 + 2 * j + 8 * x + y;
-                if (t >= lim[r] || (a.window > 0 && t < low[r] && t >= a.sinks)) s[x][y] = -INFINITY;
+                const int t = t0 + 8 * x + 2 * j + y;
+                if (t >= lim[r] || !((ok >> (x >> 1)) & 1u) || (a.window > 0 && t < low[r] && t >= a.sinks)) s[r][x][y] = -INFINITY;
               }
           }
-          float top = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+          float top = max3(s[r][0][0], s[r][0][1], s[r][1][0]);
+          top = max3(top, s[r][1][1], s[r][2][0]);
+          top = max3(top, s[r][2][1], s[r][3][0]);
+          top = fmaxf(top, s[r][3][1]);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) + vexp;
-          // the reference rises only when the tile's maximum exceeds it by
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaf(top, qs[r], vexp);
+          // the reference rises only when the step's maximum exceeds it by
           // more than kAttnSlack, so weights stay below 2^8
           const bool need = top > m_run[r] + kAttnSlack;
           if (__any_sync(0xffffffffu, need)) {
@@ -574,59 +629,108 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
             }
           }
           const float sub = m_run[r] == -INFINITY ? 0.f : vexp - m_run[r];
-          const float p00 = exp2_ftz(s[0][0] + sub), p01 = exp2_ftz(s[0][1] + sub);
-          const float p10 = exp2_ftz(s[1][0] + sub), p11 = exp2_ftz(s[1][1] + sub);
-          l_run[r] = fmaf((p00 + p01) + (p10 + p11), vdown, l_run[r]);
-          pb[r][0] = cvt_f16x2(p00 * pvs[0][0], p01 * pvs[0][1]);
-          pb[r][1] = cvt_f16x2(p10 * pvs[1][0], p11 * pvs[1][1]);
+          float sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) p[r][x][y] = exp2_ftz(fmaf(s[r][x][y], qs[r], sub));
+            sum += p[r][x][0] + p[r][x][1];
+          }
+          l_run[r] = fmaf(sum, vdown, l_run[r]);
         }
 
-        // ---- O^T += V^T P^T; the lane's value dims are 16 g + d, d = 0..15 ----
-        uint32_t r_ab = 0, r_cd = 0;
-        if constexpr (NG > 1) {
-          r_ab = cvt_f16x2(ratio[0][0], ratio[0][1]);
-          r_cd = cvt_f16x2(ratio[1][0], ratio[1][1]);
-        }
-        auto pv = [&](int i, uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {  // dims 2i, 2i + 1
-          if constexpr (NG > 1) {
-            x0 = f16x2_mul(x0, r_ab);
-            x1 = f16x2_mul(x1, r_ab);
-            y0 = f16x2_mul(y0, r_cd);
-            y1 = f16x2_mul(y1, r_cd);
-          }
+        // ---- O^T += V^T P^T, 16 keys at a time ----
 #pragma unroll
-          for (int r = 0; r < RG; ++r) mma_h16_f16(o[r][i], x0, x1, y0, y1, pb[r][0], pb[r][1]);
-        };
-        if constexpr (BITS == 4) {
-          const uint8_t* vr = st + STV + 8 * g;
-          const uint2 va = *reinterpret_cast<const uint2*>(vr + (2 * j) * VROW);
-          const uint2 vb = *reinterpret_cast<const uint2*>(vr + (2 * j + 1) * VROW);
-          const uint2 vc = *reinterpret_cast<const uint2*>(vr + (2 * j + 8) * VROW);
-          const uint2 vd = *reinterpret_cast<const uint2*>(vr + (2 * j + 9) * VROW);
+        for (int x = 0; x < 2; ++x) {
+          uint32_t pb[RG][NG][2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
-            uint32_t x[4], y[4];
-            i4x4_to_f16_tokens(__byte_perm(q < 2 ? va.x : va.y, q < 2 ? vb.x : vb.y, sel), x);
-            i4x4_to_f16_tokens(__byte_perm(q < 2 ? vc.x : vc.y, q < 2 ? vd.x : vd.y, sel), y);
-            pv(2 * q, x[0], x[1], y[0], y[1]);
-            pv(2 * q + 1, x[2], x[3], y[2], y[3]);
-          }
-        } else {
-          const uint8_t* vr = st + STV + 16 * g;
-          const uint4 va = *reinterpret_cast<const uint4*>(vr + (2 * j) * VROW);
-          const uint4 vb = *reinterpret_cast<const uint4*>(vr + (2 * j + 1) * VROW);
-          const uint4 vc = *reinterpret_cast<const uint4*>(vr + (2 * j + 8) * VROW);
-          const uint4 vd = *reinterpret_cast<const uint4*>(vr + (2 * j + 9) * VROW);
-          const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-          const uint32_t wc[4] = {vc.x, vc.y, vc.z, vc.w}, wd[4] = {vd.x, vd.y, vd.z, vd.w};
-          auto two = [](uint32_t p, uint32_t q, uint32_t sel) {
-            return f16x2_sub((__byte_perm(p, q, sel) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+          for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float v0 = vsc[(16 * x + 8 * z + 2 * j) * NG + q], v1 = vsc[(16 * x + 8 * z + 2 * j + 1) * NG + q];
+#pragma unroll
+              for (int r = 0; r < RG; ++r) pb[r][q][z] = cvt_f16x2(p[r][2 * x + z][0] * v0, p[r][2 * x + z][1] * v1);
+            }
+          const uint8_t* vt = st + ST::V + 16 * x * VROW;
+          // value columns 2 i, 2 i + 1 of the lane's 16: of keys (2j, 2j + 1)
+          // in x0, x1, of keys (2j + 8, 2j + 9) in y0, y1
+          auto pv = [&](int i, uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {
+#pragma unroll
+            for (int r = 0; r < RG; ++r) mma_h16_f16(o[r][i], x0, x1, y0, y1, pb[r][i * NG / 8][0], pb[r][i * NG / 8][1]);
           };
+          const uint8_t* row[4] = {vt + (2 * j) * VROW, vt + (2 * j + 1) * VROW, vt + (2 * j + 8) * VROW, vt + (2 * j + 9) * VROW};
+          if constexpr (BITS == 4) {
+            // four columns (16 bits) of each of the four keys
+            auto four = [&](int q, uint32_t xa, uint32_t ya) {
+              uint32_t u[4], v[4];
+              i4x4_to_f16_tokens(xa, u);
+              i4x4_to_f16_tokens(ya, v);
+              pv(2 * q, u[0], u[1], v[0], v[1]);
+              pv(2 * q + 1, u[2], u[3], v[2], v[3]);
+            };
+            if constexpr (NG == 1) {
+              uint2 v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            pv(2 * q, two(wa[q], wb[q], 0x0400), two(wa[q], wb[q], 0x0501), two(wc[q], wd[q], 0x0400), two(wc[q], wd[q], 0x0501));
-            pv(2 * q + 1, two(wa[q], wb[q], 0x0602), two(wa[q], wb[q], 0x0703), two(wc[q], wd[q], 0x0602), two(wc[q], wd[q], 0x0703));
+              for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint2*>(row[z] + 8 * g);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
+                four(q, __byte_perm(q < 2 ? v[0].x : v[0].y, q < 2 ? v[1].x : v[1].y, sel),
+                     __byte_perm(q < 2 ? v[2].x : v[2].y, q < 2 ? v[3].x : v[3].y, sel));
+              }
+            } else if constexpr (NG == 2) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint32_t v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint32_t*>(row[z] + 32 * q + 4 * g);
+                four(2 * q, __byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+                four(2 * q + 1, __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint16_t*>(row[z] + 16 * q + 2 * g);
+                four(q, v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+              }
+            }
+          } else {
+            auto two = [](uint32_t p0, uint32_t p1, uint32_t sel) {
+              return f16x2_sub((__byte_perm(p0, p1, sel) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            };
+            // four columns (32 bits) of each of the four keys
+            auto four = [&](int q, uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {
+              pv(2 * q, two(wa, wb, 0x0400), two(wa, wb, 0x0501), two(wc, wd, 0x0400), two(wc, wd, 0x0501));
+              pv(2 * q + 1, two(wa, wb, 0x0602), two(wa, wb, 0x0703), two(wc, wd, 0x0602), two(wc, wd, 0x0703));
+            };
+            if constexpr (NG == 1) {
+              uint4 v[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint4*>(row[z] + 16 * g);
+              four(0, v[0].x, v[1].x, v[2].x, v[3].x);
+              four(1, v[0].y, v[1].y, v[2].y, v[3].y);
+              four(2, v[0].z, v[1].z, v[2].z, v[3].z);
+              four(3, v[0].w, v[1].w, v[2].w, v[3].w);
+            } else if constexpr (NG == 2) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                uint2 v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint2*>(row[z] + 64 * q + 8 * g);
+                four(2 * q, v[0].x, v[1].x, v[2].x, v[3].x);
+                four(2 * q + 1, v[0].y, v[1].y, v[2].y, v[3].y);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t v[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint32_t*>(row[z] + 32 * q + 4 * g);
+                four(q, v[0], v[1], v[2], v[3]);
+              }
+            }
           }
         }
       }
@@ -645,7 +749,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
         sm.l[w][8 * r + g] = l_run[r];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // dims 16 g + 2 i, + 1 of rows 2j, 2j + 1; idx = 8 (dim & 15) + (dim >> 4)
+      for (int i = 0; i < 8; ++i) {  // columns 2 i, 2 i + 1 of the lane's 16, of rows 2j, 2j + 1
         sm.u.comb[w][8 * r + 2 * j][16 * i + g] = o[r][i][0];
         sm.u.comb[w][8 * r + 2 * j + 1][16 * i + g] = o[r][i][1];
         sm.u.comb[w][8 * r + 2 * j][16 * i + 8 + g] = o[r][i][2];
@@ -675,7 +779,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
         acc.w = fmaf(f, v.w, acc.w);
       }
       if (whole) {
-        pd_finish(a, acc, L, out_row(r), lane);
+        pd_finish<NG>(a, acc, L, out_row(r), lane);
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot + r) * kPagedDim + 4 * lane) = acc;
         if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + (slot + r) * 2) = make_float2(M, L);
@@ -725,7 +829,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 4 : 3) paged_decode_kern
           }
 #pragma unroll
           for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
-          pd_finish(a, acc, L, out_row(r), lane);
+          pd_finish<NG>(a, acc, L, out_row(r), lane);
         }
         if (tid == 0) a.counters[c0] = 0u;  // ready for the next call
       }
