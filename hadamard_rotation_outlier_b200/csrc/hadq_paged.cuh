@@ -367,18 +367,36 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t x, uint32_t y) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
+// (x & mask) ^ magic as one three-input operation.  An instruction takes one
+// constant, so the magic comes in a register the compiler cannot fold away;
+// with both as constants the codes' unpacking costs a third more.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "n"(MASK), "r"(magic));
+  return r;
+}
+// The f16 magics of the codes: biased INT4, biased INT4 times 16, biased INT8.
+struct F16Magic {
+  uint32_t m4, m4x16, m8;
+  __device__ __forceinline__ F16Magic() {
+    asm volatile("mov.u32 %0, 0x64086408;" : "=r"(m4));
+    asm volatile("mov.u32 %0, 0x64806480;" : "=r"(m4x16));
+    m8 = m4x16;
+  }
+};
 // INT4: nibble n with its sign bit flipped is code + 8; in the mantissa of
 // 1024.0 it reads 1032 + code.
-__device__ __forceinline__ void i4x8_to_f16_pairs(uint32_t w, uint32_t (&p)[4]) {
+__device__ __forceinline__ void i4x8_to_f16_pairs(uint32_t w, const F16Magic& f, uint32_t (&p)[4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = f16x2_sub(((w >> (4 * e)) & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
+  for (int e = 0; e < 4; ++e) p[e] = f16x2_sub(and_xor<0x000F000Fu>(w >> (4 * e), f.m4), f.m4);
 }
 // INT8: byte with its sign bit flipped is code + 128: 1152 + code.
-__device__ __forceinline__ void i8x8_to_f16_pairs(uint32_t lo, uint32_t hi, uint32_t (&p)[4]) {
+__device__ __forceinline__ void i8x8_to_f16_pairs(uint32_t lo, uint32_t hi, const F16Magic& f, uint32_t (&p)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t t = __byte_perm(lo, hi, uint32_t(e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12)));
-    p[e] = f16x2_sub((t & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+    p[e] = f16x2_sub(and_xor<0x00FF00FFu>(t, f.m8), f.m8);
   }
 }
 
@@ -392,6 +410,7 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const Gath
   uint32_t bm[2][2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) h16_operand(g, j, c, 0x3C00u, bm[c]);
+  const F16Magic magic;
   uint32_t flip = 0;  // bit 8 P + e: the lane's output 32 P + 8 j + e is negated
   if (a.signs) {
 #pragma unroll
@@ -440,8 +459,8 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const Gath
       uint32_t p[2][4];  // pairs (e, e + 4), e = 0..3
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if constexpr (BITS == 8) i8x8_to_f16_pairs(w[u][i].x, w[u][i].y, p[u]);
-        else i4x8_to_f16_pairs(w[u][i].x, p[u]);
+        if constexpr (BITS == 8) i8x8_to_f16_pairs(w[u][i].x, w[u][i].y, magic, p[u]);
+        else i4x8_to_f16_pairs(w[u][i].x, magic, p[u]);
       }
 #pragma unroll
       for (int o = 0; o < 2; ++o)  // bit 1 of the element

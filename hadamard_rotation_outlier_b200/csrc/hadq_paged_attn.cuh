@@ -214,6 +214,25 @@ struct __align__(16) PdSmem {
   int last;
 };
 
+template <int V>
+struct ConstInt {
+  static constexpr int value = V;
+};
+
+// 16 bytes at constant offsets from a shared and a global address.
+template <int SOFF, int GOFF>
+__device__ __forceinline__ void cp_async16_at(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(smem), "l"(gmem), "n"(SOFF), "n"(GOFF) : "memory");
+}
+// N rows TPP apart, at pitches SP and GP, from shared offset SOFF on.
+template <int N, int TPP, int SP, int GP, int SOFF, int P = 0>
+__device__ __forceinline__ void cp_rows(uint32_t smem, const void* gmem) {
+  if constexpr (P < N) {
+    cp_async16_at<SOFF + TPP * P * SP, TPP * P * GP>(smem, gmem);
+    cp_rows<N, TPP, SP, GP, SOFF, P + 1>(smem, gmem);
+  }
+}
+
 // The first of a chain of s8 products: D = A B.
 __device__ __forceinline__ void mma_s8_first(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -222,14 +241,13 @@ __device__ __forceinline__ void mma_s8_first(int (&d)[4], const uint32_t (&a)[4]
 }
 
 // 4 nibbles of two tokens (a: low half, b: high half of x) -> f16 pairs.
-__device__ __forceinline__ void i4x4_to_f16_tokens(uint32_t x, uint32_t (&r)[4]) {
+__device__ __forceinline__ void i4x4_to_f16_tokens(uint32_t x, const F16Magic& f, uint32_t (&r)[4]) {
   // 1024 + (code + 8), or 1024 + 16 (code + 8) for the odd nibbles, whose
   // sixteenth is 72 + code
   const uint32_t y = x >> 8;
-  const uint32_t t0 = (x & 0x000F000Fu) ^ 0x64086408u, t1 = (x & 0x00F000F0u) ^ 0x64806480u;
-  const uint32_t t2 = (y & 0x000F000Fu) ^ 0x64086408u, t3 = (y & 0x00F000F0u) ^ 0x64806480u;
-  r[0] = f16x2_sub(t0, 0x64086408u);
-  r[2] = f16x2_sub(t2, 0x64086408u);
+  r[0] = f16x2_sub(and_xor<0x000F000Fu>(x, f.m4), f.m4);
+  r[2] = f16x2_sub(and_xor<0x000F000Fu>(y, f.m4), f.m4);
+  const uint32_t t1 = and_xor<0x00F000F0u>(x, f.m4x16), t3 = and_xor<0x00F000F0u>(y, f.m4x16);
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(t1), "r"(0x2C002C00u), "r"(0xD480D480u));
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(t3), "r"(0x2C002C00u), "r"(0xD480D480u));
 }
@@ -257,6 +275,25 @@ __device__ __forceinline__ void warp_h128(float (&y)[4], int lane) {
   for (int m = 1; m < 32; m <<= 1) {
     const float s = (lane & m) ? -1.f : 1.f;
     lane_stage<4>(y, m, s);
+  }
+}
+
+// The scales of two consecutive keys (an even one first).
+template <int NG>
+__device__ __forceinline__ void pd_two_scales(const float* p, float (&s)[2][NG]) {
+  if constexpr (NG == 1) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    s[0][0] = v.x;
+    s[1][0] = v.y;
+  } else if constexpr (NG == 2) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    s[0][0] = v.x; s[0][1] = v.y; s[1][0] = v.z; s[1][1] = v.w;
+  } else {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 4 * y);
+      s[y][0] = v.x; s[y][1] = v.y; s[y][2] = v.z; s[y][3] = v.w;
+    }
   }
 }
 
@@ -297,6 +334,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
   extern __shared__ __align__(16) uint8_t pd_smem_raw[];
   PdSmem<RG, NG, BITS>& sm = *reinterpret_cast<PdSmem<RG, NG, BITS>*>(pd_smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+  const F16Magic magic;
 
   auto group_tiles = [&](const PagedReq& r, int rg) {
     const int f = rg * ROWS, l = min(r.rows, f + ROWS) - 1;
@@ -441,22 +479,21 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
       const uint32_t st = s_ring + uint32_t(slot_in) * ST::BYTES;
       okbits &= ~(3u << (2 * slot_in));
       const int off = key0(k) & ((1 << a.page_log2) - 1);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      auto run = [&](auto X) {
+        constexpr int x = decltype(X)::value;
         if (unsigned(pg[x]) < unsigned(a.n_pages)) {
           okbits |= 1u << (2 * slot_in + x);
           // (the rows of one tensor on one GPU are fewer than 2^32)
           const uint32_t row = ((uint32_t(pg[x]) * uint32_t(a.nkv) + uint32_t(h)) << a.page_log2) +
                                ((off + 16 * x) & ((1 << a.page_log2) - 1));
           const uint64_t at = uint64_t(row) * KROW;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            cp_async16(st + d_k + (16 * x + TPP * p) * KP, gk0 + at + TPP * p * KROW);
-            cp_async16(st + d_v + (16 * x + TPP * p) * VROW, gv0 + at + TPP * p * KROW);
-          }
-          if (lane < 8 * NG) cp_async16(st + d_s + 16 * x * 4 * NG, gs0 + uint64_t(row) * NG);
+          cp_rows<NP, TPP, KP, KROW, 16 * x * KP>(st + d_k, gk0 + at);
+          cp_rows<NP, TPP, VROW, KROW, 16 * x * VROW>(st + d_v, gv0 + at);
+          if (lane < 8 * NG) cp_async16_at<16 * x * 4 * NG, 0>(st + d_s, gs0 + uint64_t(row) * NG);
         }
-      }
+      };
+      run(ConstInt<0>{});
+      run(ConstInt<1>{});
       cp_async_commit();
       slot_in = slot_in + 1 == STAGES ? 0 : slot_in + 1;
     };
@@ -573,10 +610,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             }
           }
           float ksl[2][NG];
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int q = 0; q < NG; ++q) ksl[y][q] = ksc[(8 * x + 2 * j + y) * NG + q];
+          pd_two_scales<NG>(ksc + (8 * x + 2 * j) * NG, ksl);
 #pragma unroll
           for (int r = 0; r < RG; ++r)
 #pragma unroll
@@ -644,13 +678,14 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
         for (int x = 0; x < 2; ++x) {
           uint32_t pb[RG][NG][2];
 #pragma unroll
-          for (int q = 0; q < NG; ++q)
+          for (int z = 0; z < 2; ++z) {
+            float v[2][NG];
+            pd_two_scales<NG>(vsc + (16 * x + 8 * z + 2 * j) * NG, v);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float v0 = vsc[(16 * x + 8 * z + 2 * j) * NG + q], v1 = vsc[(16 * x + 8 * z + 2 * j + 1) * NG + q];
+            for (int q = 0; q < NG; ++q)
 #pragma unroll
-              for (int r = 0; r < RG; ++r) pb[r][q][z] = cvt_f16x2(p[r][2 * x + z][0] * v0, p[r][2 * x + z][1] * v1);
-            }
+              for (int r = 0; r < RG; ++r) pb[r][q][z] = cvt_f16x2(p[r][2 * x + z][0] * v[0][q], p[r][2 * x + z][1] * v[1][q]);
+          }
           const uint8_t* vt = st + ST::V + 16 * x * VROW;
           // value columns 2 i, 2 i + 1 of the lane's 16: of keys (2j, 2j + 1)
           // in x0, x1, of keys (2j + 8, 2j + 9) in y0, y1
@@ -663,8 +698,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             // four columns (16 bits) of each of the four keys
             auto four = [&](int q, uint32_t xa, uint32_t ya) {
               uint32_t u[4], v[4];
-              i4x4_to_f16_tokens(xa, u);
-              i4x4_to_f16_tokens(ya, v);
+              i4x4_to_f16_tokens(xa, magic, u);
+              i4x4_to_f16_tokens(ya, magic, v);
               pv(2 * q, u[0], u[1], v[0], v[1]);
               pv(2 * q + 1, u[2], u[3], v[2], v[3]);
             };
@@ -697,8 +732,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
               }
             }
           } else {
-            auto two = [](uint32_t p0, uint32_t p1, uint32_t sel) {
-              return f16x2_sub((__byte_perm(p0, p1, sel) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            auto two = [&](uint32_t p0, uint32_t p1, uint32_t sel) {
+              return f16x2_sub(and_xor<0x00FF00FFu>(__byte_perm(p0, p1, sel), magic.m8), magic.m8);
             };
             // four columns (32 bits) of each of the four keys
             auto four = [&](int q, uint32_t wa, uint32_t wb, uint32_t wc, uint32_t wd) {

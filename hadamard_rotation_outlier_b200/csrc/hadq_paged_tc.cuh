@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         dead = true;
       }
     };
+    const F16Magic magic;
     uint4 cur[NV];
     // The codes of tile n's row, once it is planned.  The second threads of
     // the rows take their eight-column pieces four further on (mod 8) than the
@@ -746,15 +747,15 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
         for (int x = 0; x < 4; ++x) {
           uint32_t p[4];
           if constexpr (BITS == 4) {
-            i4x4_to_f16_tokens(x == 0 ? cur[0].x : x == 1 ? cur[0].y : x == 2 ? cur[0].z : cur[0].w, p);
+            i4x4_to_f16_tokens(x == 0 ? cur[0].x : x == 1 ? cur[0].y : x == 2 ? cur[0].z : cur[0].w, magic, p);
           } else {
             const uint4 v = cur[x >> 1];
             const uint32_t w0 = (x & 1) ? v.z : v.x, w1 = (x & 1) ? v.w : v.y;
             // bytes with the sign bit flipped are code + 128: 1152 + code
-            p[0] = f16x2_sub((w0 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-            p[1] = f16x2_sub(((w0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-            p[2] = f16x2_sub((w1 & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
-            p[3] = f16x2_sub(((w1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+            p[0] = f16x2_sub(and_xor<0x00FF00FFu>(w0, magic.m8), magic.m8);
+            p[1] = f16x2_sub(and_xor<0x00FF00FFu>(w0 >> 8, magic.m8), magic.m8);
+            p[2] = f16x2_sub(and_xor<0x00FF00FFu>(w1, magic.m8), magic.m8);
+            p[3] = f16x2_sub(and_xor<0x00FF00FFu>(w1 >> 8, magic.m8), magic.m8);
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y) p[y] = f16x2_mul(p[y], sc[0]);
