@@ -1379,8 +1379,10 @@ constexpr size_t kPagedCounterBytes = 8192;
 static size_t paged_part_bytes(int64_t ctas, int rows) { return size_t(ctas) * 2 * rows * (hadq::kPagedDim + 2) * sizeof(float); }
 
 // Requests of up to this many query rows per KV head go to the kernel for few
-// rows.
-constexpr int kPagedFewRows = 16;
+// rows, whose time goes by rows / 16: with 32 requests of 4000 INT4 keys and 8
+// KV heads, 16 / 32 rows take 66 / 115 us there against 144 us for any count up
+// to 128 in the kernel for many (INT8, 32 rows: 126 against 151 us).
+constexpr int kPagedFewRows = 32;
 static bool paged_uses_chunk(int64_t max_rows, int g) { return max_rows > kPagedFewRows && g <= hadq::kPtRows; }
 
 static hadq_status paged_heads_check(int32_t max_new, int32_t nqh, int32_t nkv) {

@@ -191,13 +191,16 @@ constexpr int kPdTile = kPdWarps * kPdStep;     // keys per CTA and step
 constexpr int kPdPitch = kPagedDim + 4;
 
 __host__ __device__ constexpr int pd_stages(int bits) { return bits == 8 ? 2 : 3; }
-// A stage: 32 K rows, 32 V rows (pitches as in the contiguous kernel), then
-// [32][NG] K scales and as many V scales.
+// A stage: 32 K rows, 32 V rows, then [32][NG] K scales and as many V scales.
+// INT4 rows are 64 bytes, V rows at a pitch of 80; of INT8 rows, 128 bytes,
+// the 16-byte piece p of row r lies at p ^ (r & 7).  Either way the fragment
+// reads meet no bank twice, and without the contiguous kernel's padding of
+// INT8 rows a third CTA fits on an SM.
 template <int NG, int BITS>
 struct PdStage {
-  using RW = AttnRows<BITS>;
-  static constexpr int V = kPdStep * RW::KP;
-  static constexpr int S = V + kPdStep * RW::VROW;
+  static constexpr int KROW = 16 * BITS, KP = KROW, VROW = BITS == 8 ? KROW : KROW + 16;
+  static constexpr int V = kPdStep * KP;
+  static constexpr int S = V + kPdStep * VROW;
   static constexpr int BYTES = S + 2 * kPdStep * 4 * NG;
 };
 
@@ -326,9 +329,8 @@ __device__ __forceinline__ void pd_finish(const PagedAttnArgs& a, float4 acc, fl
 
 template <int RG, int NG, int BITS>
 __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kernel(const PagedAttnArgs a) {
-  using RW = AttnRows<BITS>;
   using ST = PdStage<NG, BITS>;
-  constexpr int KROW = RW::KROW, KP = RW::KP, VROW = RW::VROW;
+  constexpr int KROW = ST::KROW, KP = ST::KP, VROW = ST::VROW;
   constexpr int STAGES = pd_stages(BITS);
   constexpr int ROWS = 8 * RG;
   extern __shared__ __align__(16) uint8_t pd_smem_raw[];
@@ -466,7 +468,9 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
     constexpr int CPR = KROW / 16, TPP = 32 / CPR, NP = 16 / TPP;
     const int ctok = lane / CPR, cpart = lane % CPR;
     const uint32_t s_ring = static_cast<uint32_t>(__cvta_generic_to_shared(&sm.u.stage[w][0][0]));
-    const uint32_t d_k = ctok * KP + cpart * 16, d_v = ST::V + ctok * VROW + cpart * 16;
+    // (INT8: rows ctok + 4 p; the swizzle of odd p is that of even p with bit 2 flipped)
+    const uint32_t cdst = (BITS == 8 ? cpart ^ ctok : cpart) * 16;
+    const uint32_t d_k = ctok * KP + cdst, d_v = ST::V + ctok * VROW + cdst;
     const uint8_t* gk0 = a.k_codes + ctok * KROW + cpart * 16;
     const uint8_t* gv0 = a.v_codes + ctok * KROW + cpart * 16;
     // Scales: 4 NG pieces of 16 bytes for each run and tensor; lanes below
@@ -487,8 +491,15 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
           const uint32_t row = ((uint32_t(pg[x]) * uint32_t(a.nkv) + uint32_t(h)) << a.page_log2) +
                                ((off + 16 * x) & ((1 << a.page_log2) - 1));
           const uint64_t at = uint64_t(row) * KROW;
-          cp_rows<NP, TPP, KP, KROW, 16 * x * KP>(st + d_k, gk0 + at);
-          cp_rows<NP, TPP, VROW, KROW, 16 * x * VROW>(st + d_v, gv0 + at);
+          if constexpr (BITS == 8) {
+            cp_rows<2, 8, KP, KROW, 16 * x * KP>(st + d_k, gk0 + at);
+            cp_rows<2, 8, KP, KROW, 16 * x * KP + 4 * KP>(st + (d_k ^ 64u), gk0 + at + 4 * KROW);
+            cp_rows<2, 8, VROW, KROW, 16 * x * VROW>(st + d_v, gv0 + at);
+            cp_rows<2, 8, VROW, KROW, 16 * x * VROW + 4 * VROW>(st + (d_v ^ 64u), gv0 + at + 4 * KROW);
+          } else {
+            cp_rows<NP, TPP, KP, KROW, 16 * x * KP>(st + d_k, gk0 + at);
+            cp_rows<NP, TPP, VROW, KROW, 16 * x * VROW>(st + d_v, gv0 + at);
+          }
           if (lane < 8 * NG) cp_async16_at<16 * x * 4 * NG, 0>(st + d_s, gs0 + uint64_t(row) * NG);
         }
       };
@@ -591,13 +602,13 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
           } else {
             uint2 kw[4];
             if constexpr (NG == 1) {
-              const uint4 v0 = *reinterpret_cast<const uint4*>(kr + 32 * j);
-              const uint4 v1 = *reinterpret_cast<const uint4*>(kr + 32 * j + 16);
+              const uint4 v0 = *reinterpret_cast<const uint4*>(kr + (((2 * j) ^ g) << 4));
+              const uint4 v1 = *reinterpret_cast<const uint4*>(kr + (((2 * j + 1) ^ g) << 4));
               kw[0] = make_uint2(v0.x, v0.y); kw[1] = make_uint2(v0.z, v0.w);
               kw[2] = make_uint2(v1.x, v1.y); kw[3] = make_uint2(v1.z, v1.w);
             } else {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) kw[q] = *reinterpret_cast<const uint2*>(kr + 32 * q + 8 * j);
+              for (int q = 0; q < 4; ++q) kw[q] = *reinterpret_cast<const uint2*>(kr + (((2 * q + (j >> 1)) ^ g) << 4) + 8 * (j & 1));
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -743,7 +754,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             if constexpr (NG == 1) {
               uint4 v[4];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint4*>(row[z] + 16 * g);
+              for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint4*>(row[z] + ((g ^ (2 * j + (z & 1))) << 4));
               four(0, v[0].x, v[1].x, v[2].x, v[3].x);
               four(1, v[0].y, v[1].y, v[2].y, v[3].y);
               four(2, v[0].z, v[1].z, v[2].z, v[3].z);
@@ -753,7 +764,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
               for (int q = 0; q < 2; ++q) {
                 uint2 v[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint2*>(row[z] + 64 * q + 8 * g);
+                for (int z = 0; z < 4; ++z)
+                  v[z] = *reinterpret_cast<const uint2*>(row[z] + (((4 * q + (g >> 1)) ^ (2 * j + (z & 1))) << 4) + 8 * (g & 1));
                 four(2 * q, v[0].x, v[1].x, v[2].x, v[3].x);
                 four(2 * q + 1, v[0].y, v[1].y, v[2].y, v[3].y);
               }
@@ -762,7 +774,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
               for (int q = 0; q < 4; ++q) {
                 uint32_t v[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) v[z] = *reinterpret_cast<const uint32_t*>(row[z] + 32 * q + 4 * g);
+                for (int z = 0; z < 4; ++z)
+                  v[z] = *reinterpret_cast<const uint32_t*>(row[z] + (((2 * q + (g >> 2)) ^ (2 * j + (z & 1))) << 4) + 4 * (g & 3));
                 four(q, v[0], v[1], v[2], v[3]);
               }
             }
