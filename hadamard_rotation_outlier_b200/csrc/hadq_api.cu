@@ -1302,6 +1302,8 @@ hadq_status hadq_paged_append(const void* k, const void* v, int64_t tokens, int6
   const hadq_status st = paged_check(n_pages, page_size, n_kv_heads, dim, block, bits, group, &p);
   if (st != HADQ_OK) return st;
   if (tokens < 0) return fail(HADQ_ERR_INVALID_ARG, "tokens must be >= 0 (got %lld)", (long long)tokens);
+  if (tokens > 0x7fffffff / n_kv_heads)
+    return fail(HADQ_ERR_UNSUPPORTED, "tokens * n_kv_heads must be below 2^31 (got %lld * %d)", (long long)tokens, n_kv_heads);
   const int64_t width = int64_t(n_kv_heads) * dim;
   if (k_stride < width || v_stride < width)
     return fail(HADQ_ERR_INVALID_ARG, "k_stride and v_stride must be at least n_kv_heads * dim = %lld (got %lld, %lld)",
@@ -1326,16 +1328,16 @@ hadq_status hadq_paged_append(const void* k, const void* v, int64_t tokens, int6
   a.scales[1] = v_scales;
   a.slots = slots;
   a.signs = signs;
-  a.rows = tokens * n_kv_heads;
+  a.rows = uint32_t(tokens * n_kv_heads);
   a.nslots = p.nslots;
-  a.heads = n_kv_heads;
+  a.heads = hadq::FastDiv(uint32_t(n_kv_heads));
   a.page_log2 = p.page_log2;
   a.scale_mul = (float)(1.0 / (std::sqrt(double(dim)) * (bits == 8 ? 127.0 : 7.0)));
   const void* fn = hadq::paged_append_kernel_ptr(bits, p.ng, signs != nullptr);
   int res = 1;
   const hadq_status pst = prepare(fn, hadq::kAppendThreads, 0, "paged append kernel", &res);
   if (pst != HADQ_OK) return pst;
-  const int64_t grid = paged_wave(2 * ((a.rows + 15) / 16), hadq::kAppendThreads / 32, res);
+  const int64_t grid = paged_wave(2 * ((int64_t(a.rows) + 15) / 16), hadq::kAppendThreads / 32, res);
   return launch_paged(fn, grid, hadq::kAppendThreads, &a, 0, "paged append kernel", stream);
 }
 
@@ -1347,6 +1349,8 @@ hadq_status hadq_paged_gather(const void* codes, const float* scales, int64_t n_
   const hadq_status st = paged_check(n_pages, page_size, n_kv_heads, dim, block, bits, group, &p);
   if (st != HADQ_OK) return st;
   if (tokens < 0) return fail(HADQ_ERR_INVALID_ARG, "tokens must be >= 0 (got %lld)", (long long)tokens);
+  if (tokens > 0x7fffffff / n_kv_heads)
+    return fail(HADQ_ERR_UNSUPPORTED, "tokens * n_kv_heads must be below 2^31 (got %lld * %d)", (long long)tokens, n_kv_heads);
   if (out_dtype != HADQ_OUT_BF16 && out_dtype != HADQ_OUT_F32)
     return fail(HADQ_ERR_INVALID_ARG, "out_dtype must be HADQ_OUT_BF16 or HADQ_OUT_F32");
   if (tokens == 0 || n_pages == 0) return HADQ_OK;
@@ -1361,15 +1365,15 @@ hadq_status hadq_paged_gather(const void* codes, const float* scales, int64_t n_
   a.slots = slots;
   a.signs = signs;
   a.out = out;
-  a.rows = tokens * n_kv_heads;
+  a.rows = uint32_t(tokens * n_kv_heads);
   a.nslots = p.nslots;
-  a.heads = n_kv_heads;
+  a.heads = hadq::FastDiv(uint32_t(n_kv_heads));
   a.page_log2 = p.page_log2;
   const void* fn = hadq::paged_gather_kernel_ptr(bits, p.ng, out_dtype == HADQ_OUT_F32);
   int res = 1;
   const hadq_status pst = prepare(fn, hadq::kGatherThreads, 0, "paged gather kernel", &res);
   if (pst != HADQ_OK) return pst;
-  const int64_t grid = paged_wave((a.rows + 15) / 16, hadq::kGatherThreads / 32, res);
+  const int64_t grid = paged_wave((int64_t(a.rows) + 15) / 16, hadq::kGatherThreads / 32, res);
   return launch_paged(fn, grid, hadq::kGatherThreads, &a, 0, "paged gather kernel", stream);
 }
 

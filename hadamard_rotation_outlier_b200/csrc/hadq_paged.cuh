@@ -17,6 +17,24 @@ namespace hadq {
 
 constexpr int kPagedDim = 128;
 
+// n / d for n < 2^32 by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994, figure 4.1).
+struct FastDiv {
+  uint32_t d, m, s1, s2;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t v) : d(v) {
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < v) ++l;
+    m = uint32_t((uint64_t(1) << 32) * ((uint64_t(1) << l) - v) / v + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l < 1 ? 0 : l - 1;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return (t + ((n - t) >> s1)) >> s2;
+  }
+};
+
 // ------------------------------------------------------------------- slots
 //
 // Request b has c = cached[b] tokens in ceil(c / page) pages and gets n =
@@ -221,9 +239,10 @@ struct AppendArgs {
   float* scales[2];
   const int32_t* slots;   // [tokens]
   const int8_t* signs;    // [128] or NULL
-  int64_t rows;           // tokens * heads
+  uint32_t rows;          // tokens * heads, below 2^31
   uint32_t nslots;        // n_pages * page_size
-  int heads, page_log2;
+  int page_log2;
+  FastDiv heads;
   float scale_mul;        // 1 / (sqrt(128) * qmax)
 };
 
@@ -242,11 +261,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
 #pragma unroll
     for (int i = 0; i < 16; ++i) sm[i] = pair_sign_mask(a.signs[32 * j + 2 * i], a.signs[32 * j + 2 * i + 1]);
   }
-  const int64_t tiles = (a.rows + 15) / 16;
-  const int64_t nwarps = int64_t(gridDim.x) * (kAppendThreads / 32);
-  for (int64_t t = int64_t(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5); t < 2 * tiles; t += nwarps) {
-    const int kv = t >= tiles;
-    const int64_t r0 = (t - (kv ? tiles : 0)) * 16;
+  const uint32_t tiles = (a.rows + 15) / 16, nwarps = gridDim.x * (kAppendThreads / 32);
+  for (uint32_t t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < 2 * tiles; t += nwarps) {
+    const bool kv = t >= tiles;
+    const uint32_t r0 = (t - (kv ? tiles : 0)) * 16;
     const uint16_t* x = kv ? a.x[1] : a.x[0];
     const int64_t stride = kv ? a.stride[1] : a.stride[0];
     uint8_t* codes = kv ? a.codes[1] : a.codes[0];
@@ -255,16 +273,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     uint4 in[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t r = r0 + g + 8 * u;
+      const uint32_t r = r0 + g + 8 * u;
       dst[u] = -1;
       if (r < a.rows) {
-        const int64_t tok = r / a.heads;
-        const int head = int(r - tok * a.heads);
+        const uint32_t tok = a.heads.div(r), head = r - tok * a.heads.d;
         const uint32_t slot = uint32_t(a.slots[tok]);
         if (slot < a.nslots) {
           const uint32_t page = slot >> a.page_log2;
-          dst[u] = ((int64_t(page) * a.heads + head) << a.page_log2) + (slot - (page << a.page_log2));
-          const uint4* p = reinterpret_cast<const uint4*>(x + tok * stride + int64_t(head) * kPagedDim + 32 * j);
+          dst[u] = ((int64_t(page) * a.heads.d + head) << a.page_log2) + (slot - (page << a.page_log2));
+          const uint4* p = reinterpret_cast<const uint4*>(x + int64_t(tok) * stride + int64_t(head) * kPagedDim + 32 * j);
 #pragma unroll
           for (int i = 0; i < 4; ++i) in[u][i] = __ldg(p + i);
         }
@@ -356,11 +373,18 @@ struct GatherArgs {
   const int32_t* slots;
   const int8_t* signs;
   void* out;              // [tokens][heads][128]
-  int64_t rows;           // tokens * heads
+  uint32_t rows;          // tokens * heads, below 2^31
   uint32_t nslots;
-  int heads, page_log2;
+  int page_log2;
+  FastDiv heads;
 };
 
+// bf16x2 of (lo, hi), round to nearest even.
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // f16 pairs (low half: element e, high half: e + 4) of eight codes.
 __device__ __forceinline__ uint32_t f16x2_sub(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -417,42 +441,64 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const Gath
     for (int i = 0; i < 32; ++i)
       if (a.signs[32 * (i >> 3) + 8 * j + (i & 7)] < 0) flip |= 1u << i;
   }
-  const int64_t tiles = (a.rows + 15) / 16;
-  const int64_t nwarps = int64_t(gridDim.x) * (kGatherThreads / 32);
-  for (int64_t t = int64_t(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5); t < tiles; t += nwarps) {
-    const int64_t r0 = t * 16;
+  const uint32_t tiles = (a.rows + 15) / 16, nwarps = gridDim.x * (kGatherThreads / 32);
+  const uint32_t t_first = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5);
+  // A tile's rows are found one tile, its codes fetched one tile ahead.
+  auto find = [&](uint32_t t, int64_t (&src)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t r = t * 16 + g + 8 * u;
+      src[u] = -1;
+      if (t < tiles && r < a.rows) {
+        const uint32_t tok = a.heads.div(r), head = r - tok * a.heads.d;
+        const uint32_t slot = uint32_t(__ldg(a.slots + tok));
+        if (slot < a.nslots) {
+          const uint32_t page = slot >> a.page_log2;
+          src[u] = ((int64_t(page) * a.heads.d + head) << a.page_log2) + (slot - (page << a.page_log2));
+        }
+      }
+    }
+  };
+  float nsc[2][NG];
+  uint2 nw[2][4];
+  auto fetch = [&](const int64_t (&src)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* p = a.codes + src[u] * RB;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        nw[u][i] = make_uint2(0u, 0u);
+        if (src[u] >= 0) {
+          if constexpr (BITS == 8)
+            nw[u][i] = __ldg(reinterpret_cast<const uint2*>(p + 32 * i + 8 * j));
+          else
+            nw[u][i].x = __ldg(reinterpret_cast<const uint32_t*>(p + 16 * i + 4 * j));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < NG; ++q) nsc[u][q] = src[u] >= 0 ? __ldg(a.scales + src[u] * NG + q) : 0.f;
+    }
+  };
+  int64_t src[2], next[2];
+  find(t_first, src);
+  fetch(src);
+  find(t_first + nwarps, next);
+  for (uint32_t t = t_first; t < tiles; t += nwarps) {
+    const uint32_t r0 = t * 16;
     bool have[2];
     float sc[2][NG];
     uint2 w[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t r = r0 + g + 8 * u;
-      have[u] = false;
+      have[u] = src[u] >= 0;
+      src[u] = next[u];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[u][i] = make_uint2(0u, 0u);
+      for (int i = 0; i < 4; ++i) w[u][i] = nw[u][i];
 #pragma unroll
-      for (int q = 0; q < NG; ++q) sc[u][q] = 0.f;
-      if (r < a.rows) {
-        const int64_t tok = r / a.heads;
-        const int head = int(r - tok * a.heads);
-        const uint32_t slot = uint32_t(a.slots[tok]);
-        if (slot < a.nslots) {
-          have[u] = true;
-          const uint32_t page = slot >> a.page_log2;
-          const int64_t src = ((int64_t(page) * a.heads + head) << a.page_log2) + (slot - (page << a.page_log2));
-          const uint8_t* p = a.codes + src * RB;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (BITS == 8)
-              w[u][i] = __ldg(reinterpret_cast<const uint2*>(p + 32 * i + 8 * j));
-            else
-              w[u][i].x = __ldg(reinterpret_cast<const uint32_t*>(p + 16 * i + 4 * j));
-          }
-#pragma unroll
-          for (int q = 0; q < NG; ++q) sc[u][q] = __ldg(a.scales + src * NG + q) * kInvSqrt;
-        }
-      }
+      for (int q = 0; q < NG; ++q) sc[u][q] = nsc[u][q] * kInvSqrt;
     }
+    fetch(src);
+    find(t + 2 * nwarps, next);
     float v[2][32];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -502,7 +548,7 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const Gath
           d[1] = make_float4(x[4], x[5], x[6], x[7]);
         } else {
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + r * kPagedDim + 32 * i + 8 * j) =
-              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+              make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
         }
       }
     }
