@@ -262,35 +262,46 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     for (int i = 0; i < 16; ++i) sm[i] = pair_sign_mask(a.signs[32 * j + 2 * i], a.signs[32 * j + 2 * i + 1]);
   }
   const uint32_t tiles = (a.rows + 15) / 16, nwarps = gridDim.x * (kAppendThreads / 32);
-  for (uint32_t t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < 2 * tiles; t += nwarps) {
+  const uint32_t t_first = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  // A tile's slots are read one tile, its rows fetched one tile ahead.  K
+  // tiles first, then as many V tiles.
+  auto find = [&](uint32_t t, int64_t (&dst)[2], const uint4* (&src)[2]) {
     const bool kv = t >= tiles;
     const uint32_t r0 = (t - (kv ? tiles : 0)) * 16;
-    const uint16_t* x = kv ? a.x[1] : a.x[0];
+    const uint16_t* x = (kv ? a.x[1] : a.x[0]) + 32 * j;
     const int64_t stride = kv ? a.stride[1] : a.stride[0];
-    uint8_t* codes = kv ? a.codes[1] : a.codes[0];
-    float* scales = kv ? a.scales[1] : a.scales[0];
-    int64_t dst[2];  // row index in the pool, -1 = skip
-    uint4 in[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t r = r0 + g + 8 * u;
-      dst[u] = -1;
-      if (r < a.rows) {
+      dst[u] = -1;  // row index in the pool, -1 = skip
+      src[u] = nullptr;
+      if (t < 2 * tiles && r < a.rows) {
         const uint32_t tok = a.heads.div(r), head = r - tok * a.heads.d;
-        const uint32_t slot = uint32_t(a.slots[tok]);
+        const uint32_t slot = uint32_t(__ldg(a.slots + tok));
+        src[u] = reinterpret_cast<const uint4*>(x + int64_t(tok) * stride + int64_t(head) * kPagedDim);
         if (slot < a.nslots) {
           const uint32_t page = slot >> a.page_log2;
           dst[u] = ((int64_t(page) * a.heads.d + head) << a.page_log2) + (slot - (page << a.page_log2));
-          const uint4* p = reinterpret_cast<const uint4*>(x + int64_t(tok) * stride + int64_t(head) * kPagedDim + 32 * j);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) in[u][i] = __ldg(p + i);
         }
       }
-      if (dst[u] < 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) in[u][i] = make_uint4(0u, 0u, 0u, 0u);
-      }
     }
+  };
+  uint4 in[2][4];
+  auto fetch = [&](const uint4* const (&src)[2]) {  // (rows without a slot too: the slot may still be on its way)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[u][i] = src[u] ? __ldg(src[u] + i) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  int64_t dst[2], dnext[2];
+  const uint4* snext[2];
+  find(t_first, dst, snext);
+  fetch(snext);
+  find(t_first + nwarps, dnext, snext);
+  for (uint32_t t = t_first; t < 2 * tiles; t += nwarps) {
+    const bool kv = t >= tiles;
+    uint8_t* codes = kv ? a.codes[1] : a.codes[0];
+    float* scales = kv ? a.scales[1] : a.scales[0];
     float v[2][32];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -318,6 +329,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
           v[1][8 * i + 4 * h + 2 * c + 1] = d[3];
         }
     }
+    fetch(snext);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       reg_stage<32, 4>(v[u]);
@@ -353,6 +365,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
         *reinterpret_cast<uint4*>(codes + dst[u] * RB + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+    dst[0] = dnext[0];
+    dst[1] = dnext[1];
+    find(t + 2 * nwarps, dnext, snext);
   }
 }
 
