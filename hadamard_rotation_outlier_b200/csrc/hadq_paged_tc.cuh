@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       active = next_active;
       M = -INFINITY;
       l = 0.f;
+      bool fresh = true;  // some row of the warp has no reference
       if (active) {
         const int off = it.rq.len - it.rq.n;
         const int row = min(128 * m + r, it.ntok * a.g - 1), tok = it.first + row / a.g;
@@ -641,52 +642,59 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           uint32_t s[64];
           tmem_ld64(tS, s);
           const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
-          float x[64];
+          // The weights come first, on the reference as it stands, and no
+          // maximum is taken: a row whose weights sum to no more than 2^8 has
+          // none above it.  Where a row's do not, or it has no reference yet,
+          // the warp takes the maxima, raises references, rescales O and does
+          // the weights again.
+          uint32_t p[32];
+          float sum;
+          for (bool fix = fresh;;) {
+            float x[64];
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
-          float top0 = x[0], top1 = x[1], top2 = x[2], top3 = x[3];
+            for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(s[k]);
+            if (fix) {
+              float top = x[0];
 #pragma unroll
-          for (int k = 4; k < 60; k += 8) {
-            top0 = max3(top0, x[k], x[k + 1]);
-            top1 = max3(top1, x[k + 2], x[k + 3]);
-            top2 = max3(top2, x[k + 4], x[k + 5]);
-            top3 = max3(top3, x[k + 6], x[k + 7]);
-          }
-          top0 = max3(top0, x[60], x[61]);
-          top1 = max3(top1, x[62], x[63]);
-          const float top = fmaf(fmaxf(fmaxf(top0, top1), fmaxf(top2, top3)), f, vexp);
-          const bool need = top > M + kAttnSlack;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2f(M - top) : 1.f;
-            if (need) M = top;
-            l *= alpha;
-            if (i > i0) {
-              wait(&tl->pv_done[m], (ns - 1) & 1);  // the tile before; S came after the one before that
-              tc_fence_after();
+              for (int k = 1; k < 63; k += 2) top = max3(top, x[k], x[k + 1]);
+              top = fmaf(fmaxf(top, x[63]), f, vexp);
+              const bool need = top > M + kAttnSlack;
+              const float alpha = need ? exp2f(M - top) : 1.f;
+              if (need) M = top;
+              l *= alpha;
+              fresh = __any_sync(0xffffffffu, M == -INFINITY);
+              if (i > i0) {
+                wait(&tl->pv_done[m], (ns - 1) & 1);  // the tile before; S came after the one before that
+                tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * c, o);
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * c, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st16(tO + 16 * c, o);
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                  tmem_st16(tO + 16 * c, o);
+                }
               }
             }
-          }
-          const float sub = M == -INFINITY ? 0.f : vexp - M;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+            const float sub = M == -INFINITY ? 0.f : vexp - M;
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) fma2(x[k], x[k + 1], f, sub);
+            for (int k = 0; k < 64; k += 2) fma2(x[k], x[k + 1], f, sub);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) x[k] = exp2_ftz(x[k]);
-          uint32_t p[32];
+            for (int k = 0; k < 64; ++k) x[k] = exp2_ftz(x[k]);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (k & 1) sum2(l2, l3, x[2 * k], x[2 * k + 1]); else sum2(l0, l1, x[2 * k], x[2 * k + 1]);
-            p[k] = cvt_f16x2(x[2 * k], x[2 * k + 1]);
+            for (int k = 0; k < 32; ++k) {
+              if (k & 1) sum2(l2, l3, x[2 * k], x[2 * k + 1]); else sum2(l0, l1, x[2 * k], x[2 * k + 1]);
+              p[k] = cvt_f16x2(x[2 * k], x[2 * k + 1]);
+            }
+            sum = (l0 + l1) + (l2 + l3);
+            if (fix) break;
+            fix = __any_sync(0xffffffffu, sum > 256.f);
+            if (!fix) break;
+            tmem_ld64(tS, s);
           }
           tmem_st32(tS + 32, p);
-          l = fmaf((l0 + l1) + (l2 + l3), pow2_clamped(127 - int((info >> 8) & 255u)), l);
+          l = fmaf(sum, pow2_clamped(127 - int((info >> 8) & 255u)), l);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
