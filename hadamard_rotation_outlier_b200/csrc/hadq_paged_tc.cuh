@@ -864,14 +864,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     };
     const uint32_t qd = pt_desc_lo(qs, 16), kd = pt_desc_lo(ks, 16), vd = pt_desc_lo(vs, kPtKvHalf);
     PtIter& it = tl->it[warp];
-    const int m = warp - 16;
+    const int m = __shfl_sync(0xffffffffu, warp, 0) - 16;  // (uniform to the compiler)
     const uint32_t qm = qd + uint32_t(m) * (kPtMat >> 4), sm = uint32_t(128 * m), om = uint32_t(256 + 128 * m);
     uint32_t n = 0, ns = 0, pu = 0;  // tiles of the CTA and of the group; parity of the group's units
     auto stage = [](uint32_t t) { return t & (kPtStages - 1); };
     auto phase = [](uint32_t t) { return (t / kPtStages) & 1; };
     do {
-      const bool active = it.ntok * a.g > 128 * m;
-      const int tiles = it.i1 - it.i0;
+      const bool active = __shfl_sync(0xffffffffu, int(it.ntok * a.g > 128 * m), 0);
+      const int tiles = __shfl_sync(0xffffffffu, it.i1 - it.i0, 0);
       if (!active) {  // the stages pass unused
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i, ++n) {
