@@ -1435,6 +1435,9 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
     return fail(HADQ_ERR_UNSUPPORTED, "q_rows * n_q_heads must be below 2^31 (got %lld * %d)", (long long)q_rows, n_q_heads);
   if (max_pages > (1 << 30) / page_size)
     return fail(HADQ_ERR_UNSUPPORTED, "max_pages * page_size must be at most 2^30 (got %d * %d)", max_pages, page_size);
+  if (int64_t(p.nslots) * n_kv_heads >= int64_t(1) << 32)
+    return fail(HADQ_ERR_UNSUPPORTED, "n_pages * page_size * n_kv_heads must be below 2^32 (got %lld * %d * %d)",
+                (long long)n_pages, page_size, n_kv_heads);
   if (batch == 0 || q_rows == 0 || max_new == 0) return HADQ_OK;
   if (!q || !cu_new || !total_lens || !out || !workspace || (max_pages && !block_table) ||
       (n_pages && (!k_codes || !k_scales || !v_codes || !v_scales)))

@@ -264,9 +264,9 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// A scale as the kernels use it: one that is not finite counts as zero, so
-// that a key nobody sees cannot reach a sum.
-__device__ __forceinline__ float clean_scale(float s) { return fabsf(s) < INFINITY ? s : 0.f; }
+// A value scale as the kernels use it: one that is negative or not finite
+// counts as zero, so that a key nobody sees cannot reach a sum.
+__device__ __forceinline__ float clean_scale(float s) { return s >= 0.f && s < INFINITY ? s : 0.f; }
 
 // H_128 over idx = 4 * lane + r (bits 0-1 in registers, 2-6 on the lanes).
 __device__ __forceinline__ void warp_h128(float (&y)[4], int lane) {
@@ -279,6 +279,26 @@ __device__ __forceinline__ void warp_h128(float (&y)[4], int lane) {
     const float s = (lane & m) ? -1.f : 1.f;
     lane_stage<4>(y, m, s);
   }
+}
+
+// NG floats at an address aligned to them.
+template <int NG>
+__device__ __forceinline__ void pd_load(const float* p, float (&v)[NG]) {
+  if constexpr (NG == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else if constexpr (NG == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    v[0] = *p;
+  }
+}
+template <int NG>
+__device__ __forceinline__ void pd_store(float* p, const float (&v)[NG]) {
+  if constexpr (NG == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (NG == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else *p = v[0];
 }
 
 // The scales of two consecutive keys (an even one first).
@@ -559,15 +579,17 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
         {
           const bool there = t0 + lane < tl.kv_end && ((ok >> (lane >> 4)) & 1u);
           float v[NG], top = 0.f;
+          pd_load<NG>(vsc + lane * NG, v);
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
-            v[q] = there ? clean_scale(vsc[lane * NG + q]) : 0.f;
+            v[q] = there ? clean_scale(v[q]) : 0.f;
             top = fmaxf(top, v[q]);
           }
           ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), 27), 227);
           const float down = __uint_as_float(uint32_t(254 - ve) << 23);
 #pragma unroll
-          for (int q = 0; q < NG; ++q) vsc[lane * NG + q] = v[q] * down;
+          for (int q = 0; q < NG; ++q) v[q] *= down;
+          pd_store<NG>(vsc + lane * NG, v);
           __syncwarp();
         }
         const float vdown = __uint_as_float(uint32_t(254 - ve) << 23);  // 2^-e

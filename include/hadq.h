@@ -453,7 +453,8 @@ hadq_status hadq_paged_slots(const int32_t *cached_lens, const int32_t *new_lens
  * hadq_paged_append -- hadq_rotate_quantize of the K and V rows of new tokens,
  * written to the tokens' slots, in one launch.
  *
- *   k, v      device bf16 [tokens, n_kv_heads, dim] with k_stride (v_stride)
+ *   k, v      device bf16 [tokens, n_kv_heads, dim] (tokens * n_kv_heads
+ *             below 2^31, HADQ_ERR_UNSUPPORTED beyond) with k_stride (v_stride)
  *             elements from one token to the next, at least n_kv_heads * dim
  *             and a multiple of 8; 16-byte aligned.
  *   slots     device int32 [tokens]; a token whose slot is outside the pool is
@@ -503,8 +504,9 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *                it chooses the kernels and the workspace size, not the
  *                result.
  *   block_table  device int32 [batch, max_pages], max_pages * page_size at
- *                most 2^30.  Keys on a page outside the pool are seen by
- *                nobody.
+ *                most 2^30 (longer requests are cut to that room), the pool's
+ *                rows n_pages * page_size * n_kv_heads below 2^32.  Keys on a
+ *                page outside the pool are seen by nobody.
  *   causal       1: query i of a request with n queries and len cached tokens
  *                is at position len - n + i and sees the keys up to its own;
  *                0: every query sees all len keys.
@@ -522,8 +524,13 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *
  * Softmax statistics and sums are float32; the rotated query enters the score
  * product, and a weight the value product, with at least 11 significant bits.
- * A scale that is not finite counts as zero.  Value scales below 2^-100 (and
- * queries all of whose scaled rotated entries are) count as zero.
+ * A value scale that is negative or not finite counts as zero, and so do, next
+ * to the other keys of their tile, value scales below 2^-22 of the tile's
+ * largest (a tile is 32 or 64 keys) and scales and queries below 2^-100.  A key
+ * scale that is not finite leaves the queries that see the key unspecified, and
+ * reaches no other.
+ * A bounded wait that runs out inside the kernel for many queries is reported
+ * by hadq_device_status; the workspace has to be zero-filled again after it.
  */
 hadq_status hadq_paged_attention(const void *q, int64_t q_rows, int64_t q_stride,
                                  const int32_t *cu_new, const int32_t *total_lens, int32_t batch,
@@ -558,7 +565,8 @@ hadq_status hadq_plan(int32_t direction, int64_t rows, int32_t dim, int32_t bloc
 
 /*
  * hadq_device_status -- synchronise `stream`, then report whether any bounded
- * wait inside the library's tcgen05 kernels (HADQ_PATH_H4096_TC) ran out on
+ * wait inside the library's tcgen05 kernels (HADQ_PATH_H4096_TC, and
+ * hadq_paged_attention with more than 32 query rows per KV head) ran out on
  * the current device since the previous call, and clear the record.
  * HADQ_OK if none did; HADQ_ERR_DEVICE if one did (the outputs of the call
  * that gave up are void: every role of the kernel left its loop, waited for

@@ -252,6 +252,55 @@ def test_same_result_in_any_batch(batch):
     Case(batch, reqs, 8, 2).check(max_new=500)
 
 
+@pytest.mark.parametrize("nqh,nkv", [(200, 1), (256, 1), (300, 1), (72, 2)])
+def test_many_heads_per_kv_head(nqh, nkv):
+    """One query token of such a group fills a tile, or more than one."""
+    Case(nqh, [(1, 70), (3, 200), (2, 2)], nqh, nkv, bits=8, page=32).check()
+
+
+def test_many_requests():
+    """More requests than a CTA has threads, most of them short or empty."""
+    rng = np.random.default_rng(4)
+    reqs = [(1, int(n)) for n in rng.integers(1, 90, 300)]
+    Case(31, reqs, 2, 1).check()
+    new = rng.integers(0, 3, 900)
+    new[[5, 650, 899]] = [40, 33, 70]
+    Case(32, [(int(n), int(n) + int(c)) for n, c in zip(new, rng.integers(0, 60, 900))], 1, 1, bits=8).check()
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_pages_beyond_four_gigabytes(new):
+    """Byte offsets past 32 bits: the same bits from the far end of a pool of
+    4.3 GB codes per tensor as from a small one."""
+    c = Case(33, [(new, 300)], 2, 1, bits=4, page=16, spare_rows=0)
+    want = c.run()
+    far = (1 << 22) + 64
+    n = c.k[0].shape[0]
+    pools = []
+    for codes, scales, _ in (c.k, c.v):
+        big = torch.empty((far, 1, 16, 64), dtype=torch.uint8, device="cuda")
+        sc = torch.empty((far, 1, 16, 1), device="cuda")
+        big[far - n:], sc[far - n:] = dev(codes), dev(scales)
+        pools += [big, sc]
+    table = np.where(c.table >= 0, c.table + far - n, c.table).astype(np.int32)
+    sg = dev(c.signs)
+    out = hq.hadq_paged_attention(dev_bf16(c.q), *pools, dev(table), dev(c.lens), dev(c.cu), new, signs=sg, bits=4, group=128)
+    assert np.array_equal(host(out), want)
+    pos = np.arange(300)
+    at = dev((table[0, pos // 16] * 16 + pos % 16).astype(np.int32))
+    near = dev((c.table[0, pos // 16] * 16 + pos % 16).astype(np.int32))
+    for i, (codes, scales, _) in enumerate((c.k, c.v)):
+        assert torch.equal(hq.hadq_paged_gather(pools[2 * i], pools[2 * i + 1], at, signs=sg, bits=4, group=128),
+                           hq.hadq_paged_gather(dev(codes), dev(scales), near, signs=sg, bits=4, group=128))
+    k = dev_bf16(R.bf16(c.rng.standard_normal((300, 1, DIM))))
+    small = [torch.zeros_like(dev(a)) for a in (c.k[0], c.k[1], c.v[0], c.v[1])]
+    hq.hadq_paged_append(k, -k, near, *small, signs=sg, bits=4, group=128)
+    hq.hadq_paged_append(k, -k, at, *pools, signs=sg, bits=4, group=128)
+    used = torch.from_numpy(c.table[0][c.table[0] >= 0]).long().cuda()[:-1]  # (the last page is not full)
+    for a, b in zip(small, pools):
+        assert torch.equal(a[used], b[used + far - n])
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (64, 64), (100, 0), (100, 33), (1000, 4), (128, 500)])
 @pytest.mark.parametrize("reqs", [[(1, 1), (1, 400), (3, 260), (1, 1100)], [(150, 500), (64, 64), (1, 900), (33, 1290)]])
 def test_window_and_sinks(window, sinks, reqs):
@@ -347,6 +396,7 @@ def test_workspace_is_reused_and_left_ready():
     for _ in range(3):
         assert np.array_equal(c.run(workspace=ws), first)   # the same bits every time
     assert not ws[:8192].any()
+    B.hadq_device_status()  # no wait ran out
 
 
 def test_other_stream():

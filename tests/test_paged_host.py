@@ -62,6 +62,7 @@ CACHE = [(dict(page=8), INVALID), (dict(page=48), INVALID), (dict(page=4096), IN
     (dict(heads=0), INVALID), (dict(tokens=-1), INVALID), (dict(k_stride=255), INVALID), (dict(v_stride=128), INVALID), (dict(k=None), INVALID),
     (dict(v=None), INVALID), (dict(slots=None), INVALID), (dict(kc=None), INVALID), (dict(vs=None), INVALID), (dict(k=P + 8), MISALIGNED),
     (dict(k_stride=260), MISALIGNED), (dict(kc=P + 8), MISALIGNED), (dict(vs=P + 2), MISALIGNED), (dict(slots=P + 1), MISALIGNED),
+    (dict(tokens=1 << 30), UNSUPPORTED),
     (dict(tokens=0, k=None, v=None, slots=None), OK), (dict(pages=0, kc=None, ks=None), OK)])
 def test_append_refusals(lib, change, status):
     assert call(lib, "hadq_paged_append", APPEND, **change) == status
@@ -70,7 +71,7 @@ def test_append_refusals(lib, change, status):
 @pytest.mark.parametrize("change,status", CACHE + [
     (dict(heads=0), INVALID), (dict(tokens=-1), INVALID), (dict(dtype=2), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
     (dict(slots=None), INVALID), (dict(out=None), INVALID), (dict(codes=P + 8), MISALIGNED), (dict(out=P + 8), MISALIGNED),
-    (dict(scales=P + 1), MISALIGNED), (dict(tokens=0, out=None, codes=None), OK), (dict(pages=0, codes=None), OK)])
+    (dict(scales=P + 1), MISALIGNED), (dict(tokens=1 << 40), UNSUPPORTED), (dict(tokens=0, out=None, codes=None), OK), (dict(pages=0, codes=None), OK)])
 def test_gather_refusals(lib, change, status):
     assert call(lib, "hadq_paged_gather", GATHER, **change) == status
 
@@ -80,7 +81,8 @@ def test_gather_refusals(lib, change, status):
     (dict(max_new=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(stride=1016), INVALID), (dict(stride=1028), MISALIGNED),
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(causal=0, window=5), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=-1.0), INVALID), (dict(rows=1 << 29), UNSUPPORTED),
-    (dict(max_pages=1 << 27), UNSUPPORTED), (dict(q=None), INVALID), (dict(cu=None), INVALID), (dict(lens=None), INVALID),
+    (dict(max_pages=1 << 27), UNSUPPORTED),
+    (dict(pages=1 << 25, nkv=8), UNSUPPORTED), (dict(q=None), INVALID), (dict(cu=None), INVALID), (dict(lens=None), INVALID),
     (dict(kc=None), INVALID), (dict(vs=None), INVALID), (dict(table=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
     (dict(q=P + 8), MISALIGNED), (dict(kc=P + 8), MISALIGNED), (dict(ks=P + 4), MISALIGNED), (dict(out=P + 8), MISALIGNED),
     (dict(ws=P + 128), MISALIGNED), (dict(lens=P + 2), MISALIGNED), (dict(ws_bytes=100), INVALID), (dict(batch=0, q=None), OK),
