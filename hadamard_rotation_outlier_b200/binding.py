@@ -438,7 +438,9 @@ def _new(like, shape, dtype, stream, zero=False):
             stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
         with torch.cuda.stream(stream):
             return _new(like, shape, dtype, None, zero)
-    return like.new_zeros(shape, dtype=dtype) if zero else like.new_empty(shape, dtype=dtype)
+    if zero:
+        return like.new_zeros(shape, dtype=dtype)
+    return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
 
 
 def _at(t):
@@ -513,19 +515,16 @@ def hadq_paged_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pag
         slots = _new(cached_lens, capacity, _I32, stream)
     else:
         _on(slots, "slots", _I32, index, (slots.numel() if capacity is None else capacity,))
-    new = None
-    if total_lens is None or cu_new is None or counts is None:
-        new = _new(cached_lens, 2 * batch + 3, _I32, stream).split((batch, batch + 1, 2))
     if total_lens is None:
-        total_lens = new[0]
+        total_lens = _new(cached_lens, batch, _I32, stream)
     else:
         _on(total_lens, "total_lens", _I32, index, (batch,))
     if cu_new is None:
-        cu_new = new[1]
+        cu_new = _new(cached_lens, batch + 1, _I32, stream)
     else:
         _on(cu_new, "cu_new", _I32, index, (batch + 1,))
     if counts is None:
-        counts = new[2]
+        counts = _new(cached_lens, 2, _I32, stream)
     else:
         _on(counts, "counts", _I32, index, (2,))
     _call(lib.hadq_paged_slots, index, stream, cached_lens.data_ptr(), new_lens.data_ptr(), batch, free_pages.data_ptr(),
