@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     MAX_DIM,
     HadqError,
     hadq_dequant_rotate_inv,
+    hadq_device_status,
     hadq_dequant_rotate_inv_asym,
     hadq_dequant_rotate_inv_kron,
     hadq_dequant_rotate_inv_kron_pm1,
