@@ -343,7 +343,7 @@ __device__ __forceinline__ void pd_finish(const PagedAttnArgs& a, float4 acc, fl
     const int dim = pd_column<NG>(4 * lane + r);
     float v = y[r] * inv;
     if (a.signs && a.signs[dim] < 0) v = -v;
-    row[dim] = uint16_t(pack_bf16x2(v, 0.f));
+    row[dim] = uint16_t(bf16x2_rn(v, 0.f));  // (keeps NaN)
   }
 }
 
@@ -416,21 +416,23 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
         }
       }
       warp_h128(x, lane);
-      float amax = 0.f;
+      uint32_t top = 0;  // largest magnitude, as bits: NaN above infinity above the rest
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[i] *= a.qmul;
-        amax = fmaxf(amax, fabsf(x[i]));
+        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
       }
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      // Infinity in place of NaN: the scale multiplies the -inf of unseen keys.
+      const float amax = __uint_as_float(min(__reduce_max_sync(0xffffffffu, top), 0x7f800000u));
       // 32000 steps to the largest entry: an error of 2^-16 of it per entry.
-      // Below 2^-100 a query counts as zero.
+      // Below 2^-100 a query counts as zero; one that is not finite gets digits
+      // of zero and an infinite scale, whose product with any key is NaN.
       const bool zero = !(amax >= 7.888609e-31f);
-      const float up = zero ? 0.f : 32000.f / amax;
+      const float up = zero || amax == INFINITY ? 0.f : 32000.f / amax;
       uint32_t hi = 0, lo = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int qf = __float2int_rn(x[i] * up);
+        const int qf = up > 0.f ? __float2int_rn(x[i] * up) : 0;
         const int e1 = (qf + 128) >> 8;
         hi |= uint32_t(e1 & 0xff) << (8 * i);
         lo |= uint32_t((qf - 256 * e1) & 0xff) << (8 * i);

@@ -528,7 +528,8 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  * to the other keys of their tile, value scales below 2^-22 of the tile's
  * largest (a tile is 32 or 64 keys) and scales and queries below 2^-100.  A key
  * scale that is not finite leaves the queries that see the key unspecified, and
- * reaches no other.
+ * reaches no other.  A query that is not finite gets NaN (zeros if it sees no
+ * key) and changes no other.
  * A bounded wait that runs out inside the kernel for many queries is reported
  * by hadq_device_status; the workspace has to be zero-filled again after it.
  */

@@ -355,6 +355,31 @@ def test_nan_where_nobody_looks(new, group):
     R.check_attention(got, want, room)
 
 
+@pytest.mark.parametrize("new", [5, 60])
+@pytest.mark.parametrize("bits,group", [(4, 128), (8, 32)])
+@pytest.mark.parametrize("lens", [30, 400])
+def test_queries_that_are_not_finite(new, bits, group, lens):
+    """A query with a NaN or an infinity gets NaN, or zeros where it sees no
+    key; the rows beside it are as without it."""
+    c = Case(21, [(new, lens), (new, new - 2)], 4, 2, bits=bits, group=group)
+    c.q[1, 0, 7] = np.nan
+    c.q[2, 3] = np.nan
+    c.q[3, 1, 100] = np.inf
+    c.q[4, 2, 64] = -np.inf
+    c.q[new, 0, 5] = np.nan       # before the start: sees nothing
+    c.q[new + 1, 3, 9] = np.inf   # the same
+    got = c.run()
+    with np.errstate(invalid="ignore"):
+        want, room = R.attention(c.q, c.k, c.v, c.table, c.lens, c.cu, 16, signs=c.signs)
+    low = max(0, new - lens)      # rows of the first request before its start
+    for r, h in ((1, 0), (2, 3), (3, 1), (4, 2)):
+        if r >= low:
+            assert np.isnan(got[r, h]).all(), (r, h)
+            want[r, h] = np.nan
+    assert np.all(got[new:new + 2] == 0.0)
+    R.check_attention(got, want, room)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 @pytest.mark.parametrize("k_scale,v_scale,q_scale", [(1e-6, 1.0, 1.0), (1.0, 1e-12, 1.0), (1.0, 1e12, 1.0), (1.0, 1.0, 1e-20), (1e8, 1.0, 1e-8),
                                                      (1e-10, 1.0, 1e10), (0.0, 0.0, 1.0), (1.0, 1.0, 0.0)])
