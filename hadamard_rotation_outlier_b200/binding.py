@@ -616,7 +616,8 @@ def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch
     ``window`` and the first ``sinks`` keys.  ``workspace``: a zero-filled
     uint8 tensor of at least :func:`hadq_paged_workspace_size` bytes, reused
     across calls (one is allocated when omitted).  Returns bf16 ``[rows,
-    n_q_heads, 128]``; rows behind the last request are left as they were.
+    n_q_heads, 128]``; rows behind the last request are left as they were (of a
+    new ``out``: undefined).  ``out`` may be ``q`` itself.
     """
     lib = load_library()
     index = _cuda(q, "q")
@@ -633,6 +634,8 @@ def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch
     _on(block_table, "block_table", _I32, index)
     if signs is not None:
         _on(signs, "signs", _I8, index, (dim,))
+    if max(window, sinks, max_new) > 0x7FFFFFFF:  # (a C int would wrap)
+        raise ValueError("window, sinks and max_new must be below 2^31")
     if softmax_scale is None:
         softmax_scale = 1.0 / float(dim) ** 0.5
     if out is None:

@@ -1229,6 +1229,11 @@ static hadq_status paged_check(int64_t n_pages, int32_t page_size, int32_t n_kv_
   return HADQ_OK;
 }
 
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
+
 static hadq_status launch_paged(const void* fn, int64_t grid, int threads, void* args, size_t smem, const char* what,
                                 hadq_stream_t stream) {
   void* argv[] = {args};
@@ -1261,6 +1266,8 @@ hadq_status hadq_paged_slots(const int32_t* cached_lens, const int32_t* new_lens
   if (batch > hadq::kSlotsMaxBatch)
     return fail(HADQ_ERR_UNSUPPORTED, "batch must be at most %d (got %d)", hadq::kSlotsMaxBatch, batch);
   if (capacity > 0x7fffffff) return fail(HADQ_ERR_UNSUPPORTED, "capacity must be below 2^31");
+  if (int64_t(batch) * max_pages > 0x7fffffff)
+    return fail(HADQ_ERR_UNSUPPORTED, "batch * max_pages must be below 2^31 (got %d * %d)", batch, max_pages);
   if (!cu_new || !counts || (batch && (!cached_lens || !new_lens || !total_lens)) || (batch && max_pages && !block_table) ||
       (n_free && !free_pages) || (capacity && !slots))
     return fail(HADQ_ERR_INVALID_ARG, "the length, table, free-list and output arrays must not be NULL");
@@ -1268,8 +1275,14 @@ hadq_status hadq_paged_slots(const int32_t* cached_lens, const int32_t* new_lens
                         (const void*)block_table, (const void*)total_lens, (const void*)cu_new, (const void*)slots,
                         (const void*)counts})
     if (!aligned(p, 4)) return fail(HADQ_ERR_MISALIGNED, "every array must be 4-byte aligned");
-  if (batch && (total_lens == cached_lens || total_lens == new_lens))
-    return fail(HADQ_ERR_INVALID_ARG, "total_lens must not be one of the input arrays");
+  // Each output by itself: CTAs read the inputs while others write.
+  const struct { const void* p; int64_t n; } arr[] = {{total_lens, batch}, {cu_new, int64_t(batch) + 1}, {slots, capacity}, {counts, 2},
+                                                      {block_table, int64_t(batch) * max_pages}, {cached_lens, batch},
+                                                      {new_lens, batch}, {free_pages, n_free}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (overlap(arr[i].p, 4 * arr[i].n, arr[j].p, 4 * arr[j].n))
+        return fail(HADQ_ERR_INVALID_ARG, "an output array must not overlap another output or an input");
   hadq::SlotsArgs a{};
   a.cached = cached_lens;
   a.fresh = new_lens;
@@ -1449,6 +1462,9 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
     return fail(HADQ_ERR_MISALIGNED, "cu_new, total_lens and block_table must be 4-byte aligned");
   if (!aligned(out, 16)) return fail(HADQ_ERR_MISALIGNED, "out must be 16-byte aligned");
   if (!aligned(workspace, 256)) return fail(HADQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  const int64_t width = int64_t(n_q_heads) * dim;
+  if (!(q == out && q_stride == width) && overlap(q, ((q_rows - 1) * q_stride + width) * 2, out, q_rows * width * 2))
+    return fail(HADQ_ERR_INVALID_ARG, "out must not overlap q, unless both are the same rows");
   size_t need = 0;
   hadq_paged_workspace_size(max_new, n_q_heads, n_kv_heads, &need);
   if (workspace_bytes < need)
@@ -1475,7 +1491,7 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
   a.max_pages = max_pages;
   a.n_pages = int(n_pages);
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // (no request is longer; a position less a window stays in 32 bits)
   a.sinks = sinks;
   a.qmul = (float)(double(softmax_scale) * 1.4426950408889634 / std::sqrt(double(dim)));
   a.inv_sqrt_dim = (float)(1.0 / std::sqrt(double(dim)));

@@ -427,13 +427,14 @@ hadq_status hadq_kv_decode_attention_noalloc(const void *q, const void *k_codes,
  *   cached_lens, new_lens  device int32 [batch], batch at most 16384
  *                (HADQ_ERR_UNSUPPORTED beyond).
  *   free_pages   device int32 [n_free], the pages that may be taken.
- *   block_table  device int32 [batch, max_pages]; the entries of new pages are
+ *   block_table  device int32 [batch, max_pages] (batch * max_pages below 2^31,
+ *                HADQ_ERR_UNSUPPORTED beyond); the entries of new pages are
  *                written, all others are left as they were.
  *   total_lens   device output int32 [batch]: cached + new.  A request whose
  *                pages the free list or the table has no room for is refused:
  *                its total is 0, its slots are -1 and its table is left as it
  *                was (and so are later requests that need a page, once the
- *                free list has run out).  Not one of the input arrays.
+ *                free list has run out).
  *   cu_new       device output int32 [batch + 1]: row of each request's first
  *                new token in the packed rows of new tokens (q, k, v), and
  *                their number (the new tokens together are below 2^31).
@@ -442,6 +443,7 @@ hadq_status hadq_kv_decode_attention_noalloc(const void *q, const void *k_codes,
  *                number.  Rows at or past capacity get no slot.
  *   counts       device output int32 [2]: pages taken (the first so many of
  *                free_pages), requests refused.
+ * No output (block_table among them) may overlap another one or an input.
  */
 hadq_status hadq_paged_slots(const int32_t *cached_lens, const int32_t *new_lens, int32_t batch,
                              const int32_t *free_pages, int32_t n_free, int32_t page_size,
@@ -458,7 +460,8 @@ hadq_status hadq_paged_slots(const int32_t *cached_lens, const int32_t *new_lens
  *             elements from one token to the next, at least n_kv_heads * dim
  *             and a multiple of 8; 16-byte aligned.
  *   slots     device int32 [tokens]; a token whose slot is outside the pool is
- *             skipped.  Two tokens on one slot leave either of them there.
+ *             skipped.  The slots of two tokens differ: on one slot they leave
+ *             a mixture of both there (and touch nothing else).
  *   k_codes, k_scales, v_codes, v_scales  the pool; rows of other slots are
  *             left as they were.
  *   signs     device int8 [dim] or NULL.
@@ -515,7 +518,8 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *                lightweight QAT, streaming attention", section 3: head and
  *                local window).
  *   softmax_scale  > 0 and finite (usually 1/sqrt(dim)).
- *   out          device output bf16 [q_rows, n_q_heads, dim], 16-byte aligned.
+ *   out          device output bf16 [q_rows, n_q_heads, dim], 16-byte aligned;
+ *                q itself (with q_stride n_q_heads * dim), or apart from it.
  *                A query that sees no key gets zeros.
  *   workspace    device scratch of at least hadq_paged_workspace_size() bytes,
  *                256-byte aligned, zero-filled before its first use; every

@@ -307,6 +307,14 @@ def test_window_and_sinks(window, sinks, reqs):
     Case(window + sinks, reqs, 4, 2, bits=8).check(window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window", [2 ** 30 - 1, 2 ** 31 - 1])
+def test_window_longer_than_any_request(window):
+    """The largest windows limit nothing, queries before the start of their
+    request among them (their positions are negative)."""
+    c = Case(23, [(6, 4), (40, 10), (1, 70), (50, 300)], 4, 2)
+    assert np.array_equal(c.check(window=window)[0], c.run())
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_cross(bits):
     Case(bits, [(1, 33), (7, 1), (50, 200), (3, 0), (129, 64), (20, 1500)], 4, 4, bits=bits).check(causal=False)
@@ -422,6 +430,15 @@ def test_workspace_is_reused_and_left_ready():
         assert np.array_equal(c.run(workspace=ws), first)   # the same bits every time
     assert not ws[:8192].any()
     B.hadq_device_status()  # no wait ran out
+
+
+def test_output_in_place_of_the_queries():
+    c = Case(24, [(1, 2000), (60, 900), (3, 33)], 4, 2, spare_rows=0)
+    want = c.run()
+    q = dev_bf16(c.q)
+    args = [dev(x) for x in (c.k[0], c.k[1], c.v[0], c.v[1], c.table, c.lens, c.cu)]
+    assert hq.hadq_paged_attention(q, *args, 60, signs=dev(c.signs), out=q) is q
+    assert np.array_equal(host(q), want)
 
 
 def test_other_stream():

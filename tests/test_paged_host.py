@@ -91,6 +91,28 @@ def test_attention_refusals(lib, change, status):
     assert call(lib, "hadq_paged_attention", ATTENTION, **change) == status
 
 
+@pytest.mark.parametrize("change", [
+    dict(total=P + 4), dict(cu=2 * P + 4), dict(cu=5 * P + 4), dict(slots=6 * P + 8), dict(slots=3 * P), dict(counts=7 * P + 12), dict(counts=P),
+    dict(table=3 * P - 4), dict(table=5 * P - 60), dict(new=6 * P), dict(free=4 * P + 60)])
+def test_slots_outputs_stand_alone(lib, change):
+    """CTAs read the inputs while others write: no output may overlap an input
+    or another output, nor may it start inside one."""
+    assert call(lib, "hadq_paged_slots", SLOTS, **change) == INVALID
+    assert "overlap" in B.hadq_last_error()
+
+
+def test_slots_of_a_table_past_32_bits(lib):
+    """Page counts are summed in 32 bits."""
+    assert call(lib, "hadq_paged_slots", SLOTS, batch=16384, max_pages=1 << 17) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("change", [dict(stride=1032), dict(out=P + 16), dict(out=P + 4 * 2048 - 16), dict(out=P + 5 * 2048, stride=2048),
+                                    dict(q=P + 4 * 2048 - 16)])
+def test_attention_output_over_its_queries(lib, change):
+    assert call(lib, "hadq_paged_attention", ATTENTION, **change) == INVALID
+    assert "overlap" in B.hadq_last_error()
+
+
 def test_workspace_size(lib):
     a, b = B.hadq_paged_workspace_size(1, 32, 8), B.hadq_paged_workspace_size(2048, 32, 8)
     assert 0 < a <= b <= 48 << 20
