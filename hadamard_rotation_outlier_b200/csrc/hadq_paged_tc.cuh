@@ -2,29 +2,31 @@
 // attention): both products on the fifth-generation tensor cores.
 //
 // A unit is up to 256 query rows (two M = 128 tiles, groups 0 and 1) of one
-// request and KV head; its keys come in tiles of 128.  Per tile and group
+// request and KV head; its keys come in tiles of 64.  Per tile and group
 //     S = Q K^T    (A = Q, B = K from shared memory, S in TMEM),
-//     O += P V     (A = P in TMEM, where it overwrites S; B = V),
-// eight tcgen05.mma of K = 16 each, all operands f16:
+//     O += P V     (A = P in TMEM, beside S; B = V),
+// eight and four tcgen05.mma of K = 16 each, all operands f16:
 //  * keys and values are codes times their scale over 2^e, e the exponent of
 //    the tile's largest scale, so both fill the f16 range from the top
 //    whatever the scales are.  The scale and the product are rounded to
 //    f16: 11 bits, where the output has 8;
-//  * each rotated query is scaled by the exponent of a bound of its entries;
+//  * each rotated query is scaled by the exponent of a bound of its entries
+//    and rounded to f16;
 //  * the exponents come back as one multiplier per tile in the exponent's fma
 //    (scores) and as a summand of the softmax reference (values): with
-//    m >= max(score + e), a weight is 2^(score + e - m) <= 2^8, and l counts
-//    2^-e of it.  The reference rises only by more than 2^8, so that O, in
-//    TMEM, is rarely rescaled.  m, l and O are float32.
+//    m >= max(score + e) - 8, a weight is 2^(score + e - m) <= 2^8, rounded to
+//    f16 for the product, and l counts 2^-e of it in float32.  The reference
+//    rises only when a row's weights sum past 2^8, so that O, in TMEM, is
+//    rarely rescaled and no maximum is taken otherwise (802 -> 780 us against
+//    maxima of every tile).  m, l and O are float32.
 //
 // Roles (one CTA per SM, five warpgroups, registers dealt by setmaxnreg):
-//  * warps 0-3 and 4-7: softmax of group 0 and 1, a row per thread.  A row is
-//    read from TMEM in two halves: both for the maximum, then the second one's
-//    weights from registers and the first one's from a second read, so that a
-//    thread never holds more than half a row.  P takes the columns of S's
-//    second half.  They also rotate the next unit's queries into shared memory
-//    (H_128 in registers) before they finish a unit (rotate back, normalise,
-//    store);
+//  * warps 0-3 and 4-7: softmax of group 0 and 1, a row per thread, the 64
+//    scores in registers.  S has two buffers per group, and P takes the upper
+//    half of its own, so that S of the next tile is there when a row is done.
+//    They also rotate the next unit's queries into shared memory (on the
+//    tensor cores by mma.sync, 845 -> 802 us against H_128 in registers)
+//    before they finish a unit (rotate back, normalise, store);
 //  * warps 18 and 19 plan tiles ahead: the rows' places in the pool, their
 //    scales and the largest one's exponent;
 //  * warps 8-11 (keys) and 12-15 (values): half a cached row per thread: load
@@ -33,16 +35,21 @@
 //    bytes, and the same code);
 //  * warps 16 and 17 issue the MMAs of group 0 and 1.  Group 0's softmax runs
 //    under group 1's MMAs and the other way round.
-// The roles' loops are kept short (loops over quarters of a row instead of
-// straight code): with four instruction streams on an SM, fetching them cost
-// more than the work did (7400 cycles a tile with everything unrolled).
+// The roles' loops are kept short (run-time loops instead of straight code):
+// with four instruction streams on an SM, fetching them cost more than the
+// work did (with everything unrolled, 3700 cycles a tile).
 // The columns of Q, K, V are stored in the order in which one mask finds
 // them (pt_column): scores do not change, and H_128 of O is the same up to
 // that order, a permutation of index bits.
 //
-// Bound: 4 * 128 * 256 * 128 flops per tile pair take 2048 cycles at the dense
-// f16 rate; the 2 * 128 * 128 exponentials take as long at 16 a cycle, and
-// the operands' 256 KB of shared-memory traffic as long at 128 bytes a cycle.
+// Bound: 4 * 64 * 256 * 128 flops per tile take 1024 cycles at the dense f16
+// rate, the 2 * 128 * 64 exponentials as long at 16 a cycle, and the operands'
+// 128 KB of shared-memory traffic as long at 128 bytes a cycle.  Measured are
+// 2450 cycles a tile: 771 us for 4 requests of 1500-2048 queries x 32 heads
+// over 2000-8192 INT4 keys x 8 heads, 0.54 of cuBLAS's bf16 rate.  What fills
+// the rest is the chain of one row's softmax (read S, 64 exponentials, sum,
+// convert, write P) against which two groups hide too little, and the switch
+// between units (14,000 cycles of queries, joins and cold instructions).
 //
 // Every mbarrier wait gives up after about a second: the kernel then records a
 // fault (hadq_device_status reads it); every role runs on to its end without
@@ -347,8 +354,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // All 512 columns are this CTA's, so they start at column 0: S0, S1, O0, O1
-  // of 128 columns each, at constant addresses.
+  // All 512 columns are this CTA's, so they start at column 0, at constant
+  // addresses: S of group 0 and 1 (two buffers of 64 columns each), then O.
   constexpr uint32_t tmem = 0;
 
   if (lane == 0) {
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       return true;
     };
 
-    // Rotate back (halves as above), normalise, sign, store.
+    // Rotate back (64 columns at a time), normalise, sign, store.
     auto finish = [&]() {
       const int row = 128 * m + r;
       const bool store = row < it.ntok * a.g && !dead;
@@ -851,7 +858,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     } else {
     // ================================================================== MMAs
     // One warp per group: the control code between the issues takes as long as
-    // the products (one warp for both was busy 4500 of 5400 cycles a tile).
+    // the products (one warp for both was busy five cycles of six).
     // The whole warp walks the schedule, one lane issues.  Descriptors and
     // TMEM addresses are sums of warp-uniform bases and constants (group and
     // stage unrolled), so that an issue costs no moves to uniform registers.
