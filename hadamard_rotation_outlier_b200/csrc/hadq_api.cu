@@ -1487,6 +1487,7 @@ hadq_status hadq_paged_attention(const void* q, int64_t q_rows, int64_t q_stride
   a.nqh = n_q_heads;
   a.nkv = n_kv_heads;
   a.g = n_q_heads / n_kv_heads;
+  a.by_g = hadq::FastDiv(uint32_t(a.g));
   a.page_log2 = p.page_log2;
   a.max_pages = max_pages;
   a.n_pages = int(n_pages);

@@ -50,6 +50,7 @@ struct PagedAttnArgs {
   int causal, window, sinks;
   int row_lo, row_hi;      // this launch serves requests with row_lo < n * g <= row_hi
   int min_tiles;           // fewest key tiles a CTA takes
+  FastDiv by_g;            // division by g
   float qmul;              // softmax scale * log2(e) / sqrt(128)
   float inv_sqrt_dim;      // 1 / sqrt(128)
 };

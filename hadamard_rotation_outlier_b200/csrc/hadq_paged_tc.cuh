@@ -45,11 +45,14 @@
 // Bound: 4 * 64 * 256 * 128 flops per tile take 1024 cycles at the dense f16
 // rate, the 2 * 128 * 64 exponentials as long at 16 a cycle, and the operands'
 // 128 KB of shared-memory traffic as long at 128 bytes a cycle.  Measured are
-// 2450 cycles a tile: 771 us for 4 requests of 1500-2048 queries x 32 heads
+// 2100 cycles a tile: 760 us for 4 requests of 1500-2048 queries x 32 heads
 // over 2000-8192 INT4 keys x 8 heads, 0.54 of cuBLAS's bf16 rate.  What fills
 // the rest is the chain of one row's softmax (read S, 64 exponentials, sum,
 // convert, write P) against which two groups hide too little, and the switch
-// between units (14,000 cycles of queries, joins and cold instructions).
+// between units (17,000 cycles: 7000 for queries, 6000 for a join, 5000 to
+// finish).  The next unit's queries are therefore brought to L2 a unit ahead
+// and loaded 64 bytes of a row at a time, and rows leave in 32-byte stores (16
+// requests of 512 tokens: 156 -> 140 us, cross attention 165 -> 154 us).
 //
 // Every mbarrier wait gives up after about a second: the kernel then records a
 // fault (hadq_device_status reads it); every role runs on to its end without
@@ -296,6 +299,18 @@ __device__ __forceinline__ void sum2(float& a, float& b, float x, float y) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(A), "l"(X));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(R));
 }
+// 32 bytes in one store, or (at addresses that are multiples of 16 only) in
+// two.  A warp's stores touch a line per lane, so half as many cost half.
+__device__ __forceinline__ void pt_store32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // 2^e for any integer e (0 and the largest power of two outside the range).
 __device__ __forceinline__ float pow2_clamped(int e) {
   return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);
@@ -400,8 +415,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
     PtIter &it = tl->it[warp], &nx = tl->next[warp];
 
     // A warp rotates its 32 rows 16 at a time: four of the seven stages as an
-    // exact bf16 product with H_16 (lane (g, j) holds columns 32 j .. + 31 of
-    // rows g and g + 8, as in the append kernel), three in registers.  Each row
+    // exact bf16 product with H_16 (lane (g, j) holds columns 32 i + 8 j .. + 7,
+    // i = 0 .. 3, of rows g and g + 8, so that a load covers 64 bytes of a row),
+    // three in registers.  Each row
     // is scaled by the exponent of a bound of its entries, 128 times its
     // largest input.
     auto load_queries = [&](const PtIter& u) {
@@ -417,12 +433,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int row = 128 * m + r0 + 8 * x;
-          const int tok = row / a.g, hh = row - tok * a.g;
+          const int tok = a.by_g.div(row), hh = row - tok * a.g;
           const bool live = row < u.ntok * a.g;
           const uint4* p = reinterpret_cast<const uint4*>(
-              a.q + (live ? int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim + 32 * j : 0));
+              a.q + (live ? int64_t(u.rq.row0 + u.first + tok) * a.q_stride + int64_t(u.h * a.g + hh) * kPagedDim + 8 * j : 0));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) in[x][i] = live ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) in[x][i] = live ? __ldg(p + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t w[2][4];
-          const uint4 flip = *reinterpret_cast<const uint4*>(&tl->flip[16 * j + 4 * i]);
+          const uint4 flip = *reinterpret_cast<const uint4*>(&tl->flip[16 * i + 4 * j]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -476,14 +492,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
           for (int i = 0; i < 32; i += 2) mul2(v[x][i], v[x][i + 1], up[x]);
           const int r = r0 + 8 * x;
-          uint8_t* dst = qs + m * kPtMat + (j >> 1) * kPtHalf + r * 128;
+          uint8_t* dst = qs + m * kPtMat + r * 128;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               w[k] = cvt_f16x2(v[x][8 * i + pt_column<BITS>(2 * k)], v[x][8 * i + pt_column<BITS>(2 * k + 1)]);
-            *reinterpret_cast<uint4*>(dst + (((4 * (j & 1) + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + (i >> 1) * kPtHalf + (((4 * (i & 1) + j) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
@@ -559,7 +575,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       const int row = 128 * m + r;
       const bool store = row < it.ntok * a.g && !dead;
       const float inv = l > 0.f ? a.inv_sqrt_dim * 0.0078125f / l : 0.f;  // values entered times 2^7
-      const int tok = row / a.g, hh = row - tok * a.g;
+      const int tok = a.by_g.div(row), hh = row - tok * a.g;
+      const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
       uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(it.rq.row0 + it.first + tok) * a.nqh + it.h * a.g + hh) * kPagedDim);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -578,13 +595,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
           for (int k = 0; k < 64; k += 2) mul2(y[k], y[k + 1], inv);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 flip = *reinterpret_cast<const uint4*>(&tl->flip[32 * h + 4 * c]);
-            const float* z = y + 8 * c;
-            dst[8 * h + c] = make_uint4(cvt_bf16x2(z[pt_position<BITS>(0)], z[pt_position<BITS>(1)]) ^ flip.x,
-                                        cvt_bf16x2(z[pt_position<BITS>(2)], z[pt_position<BITS>(3)]) ^ flip.y,
-                                        cvt_bf16x2(z[pt_position<BITS>(4)], z[pt_position<BITS>(5)]) ^ flip.z,
-                                        cvt_bf16x2(z[pt_position<BITS>(6)], z[pt_position<BITS>(7)]) ^ flip.w);
+          for (int c = 0; c < 4; ++c) {  // 16 columns, 32 bytes
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float* z = y + 16 * c + 8 * (k >> 2);
+              w[k] = cvt_bf16x2(z[pt_position<BITS>(2 * (k & 3))], z[pt_position<BITS>(2 * (k & 3) + 1)]) ^ tl->flip[32 * h + 8 * c + k];
+            }
+            pt_store32(dst + 8 * h + 2 * c, w, wide);
           }
         }
       }
@@ -607,17 +625,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       __syncwarp();
       if (lane == 0) it = nx;
       more = nx.warp_next(a, per);  // (looked up while this unit runs)
+      if (more && 128 * m + r < nx.ntok * a.g) {  // its queries to L2: a row per thread
+        const int row = 128 * m + r, tok = a.by_g.div(row);
+        const uint16_t* p = a.q + int64_t(nx.rq.row0 + nx.first + tok) * a.q_stride + int64_t(nx.h * a.g + row - tok * a.g) * kPagedDim;
+        asm volatile("prefetch.global.L2 [%0];\n prefetch.global.L2 [%0 + 128];" ::"l"(p));
+      }
       active = next_active;
       M = -INFINITY;
       l = 0.f;
       bool fresh = true;  // some row of the warp has no reference
       if (active) {
         const int off = it.rq.len - it.rq.n;
-        const int row = min(128 * m + r, it.ntok * a.g - 1), tok = it.first + row / a.g;
+        const int row = min(128 * m + r, it.ntok * a.g - 1), tok = it.first + int(a.by_g.div(row));
         const int lim = a.causal ? min(it.rq.len, off + tok + 1) : it.rq.len;
         const int low = a.window > 0 ? off + tok - a.window + 1 : 0;
         // keys that every row of the group sees: below all_lim, from all_low on
-        const int f_tok = it.first + 128 * m / a.g, l_tok = it.first + min(128 * m + 127, it.ntok * a.g - 1) / a.g;
+        const int f_tok = it.first + int(a.by_g.div(128 * m)), l_tok = it.first + int(a.by_g.div(min(128 * m + 127, it.ntok * a.g - 1)));
         const int all_lim = a.causal ? off + f_tok + 1 : it.rq.len;
         const int all_low = a.window > 0 ? off + l_tok - a.window + 1 : 0;
         const int i0 = it.i0, i1 = it.i1, head = it.tl.head, from = it.tl.from - head;

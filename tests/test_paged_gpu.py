@@ -441,6 +441,26 @@ def test_output_in_place_of_the_queries():
     assert np.array_equal(host(q), want)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_rows_aligned_to_16_bytes_only(bits):
+    """q and out that start 16 bytes behind a 32-byte boundary."""
+    c = Case(25, [(1, 200), (70, 300), (200, 210)], 4, 2, bits=bits, spare_rows=2)
+    want = c.run()
+    n = c.q.size
+
+    def behind(fill):
+        t = torch.full((n + 16,), fill, dtype=torch.bfloat16, device="cuda")
+        return t, t[8:8 + n].view(c.q.shape)
+
+    (qb, q), (ob, out) = behind(0.0), behind(99.0)
+    q.copy_(dev_bf16(c.q))
+    assert q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    args = [dev(x) for x in (c.k[0], c.k[1], c.v[0], c.v[1], c.table, c.lens, c.cu)]
+    hq.hadq_paged_attention(q, *args, 200, signs=dev(c.signs), bits=bits, out=out)
+    assert np.array_equal(host(out), want)
+    assert np.all(host(ob[:8]) == 99.0) and np.all(host(ob[8 + n:]) == 99.0)
+
+
 def test_other_stream():
     c = Case(15, [(1, 300), (20, 300)], 4, 2)
     want = c.run()
