@@ -179,8 +179,8 @@ __device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPl
 //    them.  No shuffle but the two of the row maximum.
 // A weight enters as f16 times its value scale over 2^e, e the exponent of the
 // largest value scale among the 32 keys, and the running reference counts e
-// in: m = max(score + e), so an f16 weight is at most 2^9 whatever the scales
-// are (11 bits kept, against the 8 of the bf16 output); l and O are float32.
+// in: m = max(score + e) - 8 when it was last raised, so an f16 weight is below
+// 2^15 whatever the scales are; l and O are float32.
 //
 // Bound by HBM for long INT8 caches and by the issue rate for INT4: a cached
 // row pair is 2 * (16 BITS + 512 / G) bytes against about 13 warp
@@ -206,6 +206,16 @@ struct PdStage {
   static constexpr int S = V + kPdStep * VROW;
   static constexpr int BYTES = S + 2 * kPdStep * 4 * NG;
 };
+
+// Weights are held in f16 for the value product, so the reference stays
+// kPagedRoom below the largest score + e it has met: a weight down to 2^-22 of
+// the largest keeps 11 bits (the bf16 output has 8), and one below that an
+// error of 2^-33 of the largest.  It takes that many where one key that adds
+// nothing (a sink whose value is near zero) holds nearly all weight, and the
+// output is the rest of a long cache: 2047 keys at 2^-24 each came out several
+// percent off with the reference at the largest score.
+constexpr float kPagedRoom = 8.f;
+constexpr float kPdSlack = 5.5f;  // log2 units a score may pass the reference's before that is raised
 
 template <int RG, int NG, int BITS>
 struct __align__(16) PdSmem {
@@ -682,10 +692,10 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
           top = fmaxf(top, s[r][3][1]);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          top = fmaf(top, qs[r], vexp);
-          // the reference rises only when the step's maximum exceeds it by
-          // more than kAttnSlack, so weights stay below 2^8
-          const bool need = top > m_run[r] + kAttnSlack;
+          top = fmaf(top, qs[r], vexp - kPagedRoom);
+          // the reference rises only when the step's maximum asks for more than
+          // kPdSlack, so weights stay below 2^13.5
+          const bool need = top > m_run[r] + kPdSlack;
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? exp2f(m_run[r] - top) : 1.f;
             if (need) m_run[r] = top;

@@ -14,11 +14,12 @@
 //    and rounded to f16;
 //  * the exponents come back as one multiplier per tile in the exponent's fma
 //    (scores) and as a summand of the softmax reference (values): with
-//    m >= max(score + e) - 8, a weight is 2^(score + e - m) <= 2^8, rounded to
-//    f16 for the product, and l counts 2^-e of it in float32.  The reference
-//    rises only when a row's weights sum past 2^8, so that O, in TMEM, is
-//    rarely rescaled and no maximum is taken otherwise (802 -> 780 us against
-//    maxima of every tile).  m, l and O are float32.
+//    m = max(score + e) - 8 when it was last raised, a weight is 2^(score + e - m),
+//    rounded to f16 for the product (kPagedRoom), and l counts 2^-e of it in
+//    float32.  The reference rises only when a row's weights sum past f16's
+//    largest number, so that O, in TMEM, is rarely rescaled and no maximum is
+//    taken otherwise (802 -> 780 us against maxima of every tile).  m, l and O
+//    are float32.
 //
 // Roles (one CTA per SM, five warpgroups, registers dealt by setmaxnreg):
 //  * warps 0-3 and 4-7: softmax of group 0 and 1, a row per thread, the 64
@@ -79,6 +80,8 @@ constexpr int kPtKvHalf = 64 * 128, kPtKv = 2 * kPtKvHalf;  // the same of a til
 constexpr int kPtPlans = 4;   // tiles whose rows and scales are worked out ahead
 constexpr int kPtInfos = 16;  // tiles whose info the softmax may still need: 2 ahead of it in S, 4 in K, 4 planned
 constexpr int kPtMaxCtas = 160;
+constexpr float kPtWeights = 65504.f;  // a row's weights of a tile: f16's largest number
+constexpr float kPtSlack = 7.f;        // log2 units its reference may trail then: weights stay below 2^15
 constexpr int kPtCounterBase = 1024;          // first of this kernel's arrival counters
 
 // Instruction descriptors: D float32, A and B f16, M = 128.
@@ -673,10 +676,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           tmem_ld64(tS, s);
           const float f = pow2_clamped(int(info & 255u) - 134 - eq), vexp = float(int((info >> 8) & 255u) - 127);
           // The weights come first, on the reference as it stands, and no
-          // maximum is taken: a row whose weights sum to no more than 2^8 has
-          // none above it.  Where a row's do not, or it has no reference yet,
-          // the warp takes the maxima, raises references, rescales O and does
-          // the weights again.
+          // maximum is taken: a row whose weights sum to no more than
+          // kPtWeights has none above it.  Where a row's do not, or it has no
+          // reference yet, the warp takes the maxima, raises references,
+          // rescales O and does the weights again.
           uint32_t p[32];
           float sum;
           for (bool fix = fresh;;) {
@@ -687,8 +690,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
               float top = x[0];
 #pragma unroll
               for (int k = 1; k < 63; k += 2) top = max3(top, x[k], x[k + 1]);
-              top = fmaf(fmaxf(top, x[63]), f, vexp);
-              const bool need = top > M + kAttnSlack;
+              top = fmaf(fmaxf(top, x[63]), f, vexp - kPagedRoom);
+              const bool need = top > M + kPtSlack;
               const float alpha = need ? exp2f(M - top) : 1.f;
               if (need) M = top;
               l *= alpha;
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             }
             sum = (l0 + l1) + (l2 + l3);
             if (fix) break;
-            fix = __any_sync(0xffffffffu, sum > 256.f);
+            fix = __any_sync(0xffffffffu, sum > kPtWeights);
             if (!fix) break;
             tmem_ld64(tS, s);
           }

@@ -527,7 +527,9 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *                be ordered (also two captured graphs that do).
  *
  * Softmax statistics and sums are float32; the rotated query enters the score
- * product, and a weight the value product, with at least 11 significant bits.
+ * product with at least 11 significant bits.  A weight enters the value product
+ * with 11 significant bits down to 2^-22 of its row's largest, and with an error
+ * of 2^-33 of the largest below that.
  * A value scale that is negative or not finite counts as zero, and so do, next
  * to the other keys of their tile, value scales below 2^-22 of the tile's
  * largest (a tile is 32 or 64 keys) and scales and queries below 2^-100.  A key

@@ -1,0 +1,40 @@
+"""Paged attention over caches and queries of extreme size: value scales that
+span the float32 range, keys that take nearly all weight, signed key scales,
+queries that are not finite."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_paged_bounds_gpu import held
+from test_paged_gpu import Case
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+
+# ------------------------------------------- nearly all weight on one key
+
+def one_loud_key(c, gap, value):
+    """Key 0 of every request has a score `gap` log2 units above the others',
+    which are near zero; its value row is `value` times as large."""
+    c.signs = None
+    c.q[:] = 0.0
+    c.k[1][:] *= 2.0 ** -5
+    c.q[..., 0] = 8.0                                # rotated: 8 / sqrt(128) in every column
+    for b in range(len(c.lens)):
+        p = c.table[b, 0]
+        c.k[0][p, :, 0] = 0x77 if c.bits == 4 else 127
+        c.k[1][p, :, 0] = gap * np.log(2.0) / ((7 if c.bits == 4 else 127) * 8.0)   # 128 columns, times 1 / sqrt(128) twice
+        c.v[1][p, :, 0] *= value
+
+
+@pytest.mark.parametrize("gap,value", [(20, 0.0), (24, 0.0), (24, 2.0 ** -6)])
+@pytest.mark.parametrize("new,lens,batch,heads", [(1, 2048, 60, 8), (33, 4096, 4, 4)])
+def test_one_key_with_nearly_all_weight(gap, value, new, lens, batch, heads):
+    """A sink: what it adds to the output is nothing, or little, and the output
+    is made of weights down to 2^-24 of its own.  (Enough requests for one CTA
+    to see the sink and thousands of other keys of its request.)"""
+    c = Case(gap, [(new, lens)] * batch, heads, heads, page=64, bits=4)
+    one_loud_key(c, gap, value)
+    held(c)
