@@ -217,6 +217,16 @@ struct PdStage {
 constexpr float kPagedRoom = 8.f;
 constexpr float kPdSlack = 5.5f;  // log2 units a score may pass the reference's before that is raised
 
+// The exponent e of a tile's value scales (biased by 127) goes into the
+// reference, and l counts a weight as 2^(score + e - m) 2^-e.  For that product
+// to hold on to a key whose e is far from the other tiles', e stays at or above
+// 2^-80 (l then ends below 2^(80 + 14 + 30)) and, within a unit, no more than
+// kPagedExpSpan below the largest so far: a tile of zero value rows still
+// counts in l after one of large ones.  Two references may lie 200 apart all
+// the same, so sums go from one to the other by the root of the factor, twice.
+constexpr int kPagedExpLow = 127 - 80;
+constexpr int kPagedExpSpan = 40;
+
 template <int RG, int NG, int BITS>
 struct __align__(16) PdSmem {
   union {
@@ -546,6 +556,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
 
     float o[RG][8][4];
     float m_run[RG], l_run[RG];
+    int ve_low = kPagedExpLow;  // of the next step
 #pragma unroll
     for (int k = 0; k < RG; ++k) {
 #pragma unroll
@@ -600,7 +611,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             v[q] = there ? clean_scale(v[q]) : 0.f;
             top = fmaxf(top, v[q]);
           }
-          ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), 27), 227);
+          ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), ve_low), 227);
+          ve_low = max(ve_low, ve - kPagedExpSpan);
           const float down = __uint_as_float(uint32_t(254 - ve) << 23);
 #pragma unroll
           for (int q = 0; q < NG; ++q) v[q] *= down;
@@ -697,9 +709,9 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
           // kPdSlack, so weights stay below 2^13.5
           const bool need = top > m_run[r] + kPdSlack;
           if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2f(m_run[r] - top) : 1.f;
+            const float root = need ? exp2f(0.5f * (m_run[r] - top)) : 1.f, alpha = root * root;
             if (need) m_run[r] = top;
-            l_run[r] *= alpha;
+            l_run[r] = l_run[r] * root * root;
             // accumulators of this lane belong to rows 2j, 2j + 1
             const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * j), a1 = __shfl_sync(0xffffffffu, alpha, 8 * j + 4);
 #pragma unroll
@@ -855,8 +867,8 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kPdWarps; ++x) {
-        const float f = sm.m[x][r] == -INFINITY ? 0.f : exp2f(sm.m[x][r] - M);
-        L = fmaf(f, sm.l[x][r], L);
+        const float root = sm.m[x][r] == -INFINITY ? 0.f : exp2f(0.5f * (sm.m[x][r] - M)), f = root * root;
+        L = fmaf(root, root * sm.l[x][r], L);
         const float4 v = *reinterpret_cast<const float4*>(&sm.u.comb[x][r][4 * lane]);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
@@ -891,8 +903,9 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             float f = 0.f;
             if (base + lane <= c1) {
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at_of(base + lane) * 2));
-              f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-              L = fmaf(f, ml.y, L);
+              const float root = ml.x == -INFINITY ? 0.f : exp2f(0.5f * (ml.x - M));
+              f = root * root;
+              L = fmaf(root, root * ml.y, L);
             }
             const int n = min(32, c1 - base + 1);
             for (int x = 0; x < n; x += 8) {

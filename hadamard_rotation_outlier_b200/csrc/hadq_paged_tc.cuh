@@ -143,7 +143,7 @@ struct PtTail {
   uint64_t k_full[kPtStages], k_empty[kPtStages], v_full[kPtStages], v_empty[kPtStages];
   uint64_t plan_full[kPtPlans], plan_empty[kPtPlans];
   uint32_t info[kPtInfos];   // of the last tiles: exponents of the largest K scale (bits 0-7) and V scale
-                             // (8-15), whether every key is cached (16)
+                             // (8-15), whether every key is cached (16), lower limit of the next V one (24-31)
   uint32_t ok[kPtInfos][2];  // the tile's keys that are cached
   uint32_t row[kPtPlans][kPtTile];       // rows of the tile's keys in the pool, ~0: not cached
   uint32_t scale[kPtPlans][2][4][kPtTile];  // K and V scales over 2^e as f16 pairs, by group
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll 1
         for (int x = c0; x <= c1; ++x) {
           const float2 ml = __ldcg(&pm[slot(x) * kPtRows + row]);
-          const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-          if (q == 0) l = fmaf(w, ml.y, l);
+          const float root = ml.x == -INFINITY ? 0.f : exp2f(0.5f * (ml.x - M)), w = root * root;
+          if (q == 0) l = fmaf(root, root * ml.y, l);
           const float4* px = po + (slot(x) * 32 + 8 * q) * kPtRows + row;
           float4 v[8];
 #pragma unroll
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           wait(&tl->s_full[m][h], (ns >> 1) & 1);
           tc_fence_after();
           const uint32_t info = tl->info[n % kPtInfos];
-          masked |= (info >> 16) == 0;
+          masked |= (info & 0x10000u) == 0;
           if (masked) {  // put -inf where a row sees nothing
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -692,9 +692,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
               for (int k = 1; k < 63; k += 2) top = max3(top, x[k], x[k + 1]);
               top = fmaf(fmaxf(top, x[63]), f, vexp - kPagedRoom);
               const bool need = top > M + kPtSlack;
-              const float alpha = need ? exp2f(M - top) : 1.f;
+              const float root = need ? exp2f(0.5f * (M - top)) : 1.f, alpha = root * root;
               if (need) M = top;
-              l *= alpha;
+              l = l * root * root;
               fresh = __any_sync(0xffffffffu, M == -INFINITY);
               if (i > i0) {
                 wait(&tl->pv_done[m], (ns - 1) & 1);  // the tile before; S came after the one before that
@@ -821,6 +821,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
       // Two warps, every other tile each: where the tile's rows are, their
       // scales, the largest one's exponent.  Two keys per lane.
       bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!pt_wait(bar, parity, abort)) {
+          if (!dead) tc_give_up(&tl->abort, fault);
+          dead = true;
+        }
+      };
       PtIter& it = tl->it[warp];
       int i = it.i0;
       const uint32_t total = uint32_t(pc.end - pc.at);
@@ -853,11 +859,15 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           int e[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), 227);
-          const uint32_t ok0 = __ballot_sync(0xffffffffu, row[0] != ~0u), ok1 = __ballot_sync(0xffffffffu, row[1] != ~0u);
-          if (!pt_wait(&tl->plan_empty[sl], ((n / kPtPlans) & 1) ^ 1u, abort)) {
-            if (!dead) tc_give_up(&tl->abort, fault);
-            dead = true;
+          int low = kPagedExpLow;
+          if (i > it.i0) {  // the tile before, of the other warp (which publishes no further one before this)
+            wait(&tl->plan_full[(n - 1) % kPtPlans], ((n - 1) / kPtPlans) & 1);
+            low = int(tl->info[(n - 1) % kPtInfos] >> 24);
           }
+          e[1] = max(e[1], low);
+          low = max(low, e[1] - kPagedExpSpan);
+          const uint32_t ok0 = __ballot_sync(0xffffffffu, row[0] != ~0u), ok1 = __ballot_sync(0xffffffffu, row[1] != ~0u);
+          wait(&tl->plan_empty[sl], ((n / kPtPlans) & 1) ^ 1u);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             tl->row[sl][lane + 32 * x] = row[x];
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           if (lane == 0) {
             tl->ok[n % kPtInfos][0] = ok0;
             tl->ok[n % kPtInfos][1] = ok1;
-            tl->info[n % kPtInfos] = uint32_t(e[0]) | (uint32_t(e[1]) << 8) | ((ok0 & ok1) == ~0u ? 1u << 16 : 0u);
+            tl->info[n % kPtInfos] = uint32_t(e[0]) | (uint32_t(e[1]) << 8) | ((ok0 & ok1) == ~0u ? 1u << 16 : 0u) | (uint32_t(low) << 24);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&tl->plan_full[sl]);

@@ -531,9 +531,10 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  * with 11 significant bits down to 2^-22 of its row's largest, and with an error
  * of 2^-33 of the largest below that.
  * A value scale that is negative or not finite counts as zero, and so do, next
- * to the other keys of their tile, value scales below 2^-22 of the tile's
- * largest (a tile is 32 or 64 keys) and scales and queries below 2^-100.  A key
- * scale that is not finite leaves the queries that see the key unspecified, and
+ * to the other keys, value scales below 2^-22 of the largest in their tile (32
+ * or 64 keys) or below 2^-60 of the largest in their request, and scales and
+ * queries below 2^-100; such a key keeps its weight in the sum.  A key scale
+ * that is not finite leaves the queries that see the key unspecified, and
  * reaches no other.  A query that is not finite gets NaN (zeros if it sees no
  * key) and changes no other.
  * A bounded wait that runs out inside the kernel for many queries is reported

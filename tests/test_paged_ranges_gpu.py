@@ -13,6 +13,52 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
 
+NONE = None  # value scales of zero
+SPANS = {
+    "zeros behind": [30, NONE, NONE, NONE],
+    "zeros before": [NONE, 30],
+    "zeros far behind": [100, NONE, NONE],
+    "tiny behind": [60, -60, -90],
+    "tiny before": [-90, 96],
+    "up and down": [-60, 40, 0, 90, -90, NONE, 20],
+    "one size": [-85],
+    "down": [90, 50, 10, -30, -70],
+}
+
+
+def spans(c, blocks):
+    """Value scales times 2^e, e by blocks of 128 keys."""
+    scales = c.v[1]
+    for b, n in enumerate(c.lens):
+        for pos in range(0, n, c.page):
+            e = blocks[(pos // 128) % len(blocks)]
+            scales[c.table[b, pos // c.page]] *= 0.0 if e is NONE else 2.0 ** e
+
+
+@pytest.mark.parametrize("name", SPANS)
+@pytest.mark.parametrize("quiet", [True, False])
+@pytest.mark.parametrize("new", [1, 40])
+def test_value_scales_that_span(name, quiet, new):
+    """Keys hold their part of the weight whatever their values' size: with
+    scores of zero (quiet) the output is the plain mean."""
+    few = new == 1
+    c = Case(len(name) + new, [(new, 1024 - 37 * b % 400) for b in range(56 if few else 10)], 8 if few else 2, 8 if few else 2,
+             page=64, bits=8, group=64 if quiet else 128)
+    spans(c, SPANS[name])
+    if quiet:
+        c.k[1][:] = 0.0
+    held(c)
+
+
+def test_value_scales_join():
+    """The same over one request that all CTAs share."""
+    for new, lens in ((1, 20000), (40, 3000)):
+        for name in SPANS:
+            c = Case(len(name) + new, [(new, lens)], 2, 1, page=64, bits=4)
+            spans(c, SPANS[name])
+            held(c)
+
+
 # ------------------------------------------- nearly all weight on one key
 
 def one_loud_key(c, gap, value):
