@@ -180,7 +180,7 @@ __device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPl
 // A weight enters as f16 times its value scale over 2^e, e the exponent of the
 // largest value scale among the 32 keys, and the running reference counts e
 // in: m = max(score + e) - 8 when it was last raised, so an f16 weight is below
-// 2^15 whatever the scales are; l and O are float32.
+// 2^16 whatever the scales are; l and O are float32.
 //
 // Bound by HBM for long INT8 caches and by the issue rate for INT4: a cached
 // row pair is 2 * (16 BITS + 512 / G) bytes against about 13 warp
@@ -225,6 +225,7 @@ constexpr float kPdSlack = 5.5f;  // log2 units a score may pass the reference's
 // counts in l after one of large ones.  Two references may lie 200 apart all
 // the same, so sums go from one to the other by the root of the factor, twice.
 constexpr int kPagedExpLow = 127 - 80;
+constexpr int kPagedExpHigh = 127 + 126;  // (2^-e is a normal number)
 constexpr int kPagedExpSpan = 40;
 
 template <int RG, int NG, int BITS>
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(kPdThreads, RG == 1 ? 3 : 2) paged_decode_kern
             v[q] = there ? clean_scale(v[q]) : 0.f;
             top = fmaxf(top, v[q]);
           }
-          ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), ve_low), 227);
+          ve = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23), ve_low), kPagedExpHigh);
           ve_low = max(ve_low, ve - kPagedExpSpan);
           const float down = __uint_as_float(uint32_t(254 - ve) << 23);
 #pragma unroll

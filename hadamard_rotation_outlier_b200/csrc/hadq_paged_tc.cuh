@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
             }
           int e[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), 227);
+          for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), y ? kPagedExpHigh : 227);
           int low = kPagedExpLow;
           if (i > it.i0) {  // the tile before, of the other warp (which publishes no further one before this)
             wait(&tl->plan_full[(n - 1) % kPtPlans], ((n - 1) / kPtPlans) & 1);

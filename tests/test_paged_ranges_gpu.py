@@ -84,3 +84,15 @@ def test_one_key_with_nearly_all_weight(gap, value, new, lens, batch, heads):
     c = Case(gap, [(new, lens)] * batch, heads, heads, page=64, bits=4)
     one_loud_key(c, gap, value)
     held(c)
+
+
+# ---------------------------------------------------- large value scales
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("e", [99, 103, 118])
+def test_large_value_scales(new, bits, e):
+    """Value rows up to the largest that bf16 holds."""
+    c = Case(43, [(new, 300), (new, 90)], 4, 2, bits=bits)
+    c.v[1][:] *= np.float32(2.0 ** e)
+    held(c)
