@@ -851,9 +851,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int q = 0; q < NG; ++q) {
-              sc[0][x][q] = row[x] != ~0u ? clean_scale(__ldg(a.k_scales + int64_t(row[x]) * NG + q)) : 0.f;
+              const float k = row[x] != ~0u ? __ldg(a.k_scales + int64_t(row[x]) * NG + q) : 0.f;
+              sc[0][x][q] = fabsf(k) < INFINITY ? k : 0.f;  // (signed; what one that is not finite gives is open)
               sc[1][x][q] = row[x] != ~0u ? clean_scale(__ldg(a.v_scales + int64_t(row[x]) * NG + q)) : 0.f;
-              top[0] = fmaxf(top[0], sc[0][x][q]);
+              top[0] = fmaxf(top[0], fabsf(sc[0][x][q]));
               top[1] = fmaxf(top[1], sc[1][x][q]);
             }
           int e[2];

@@ -534,9 +534,9 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  * to the other keys, value scales below 2^-22 of the largest in their tile (32
  * or 64 keys) or below 2^-60 of the largest in their request, and scales and
  * queries below 2^-100; such a key keeps its weight in the sum.  A key scale
- * that is not finite leaves the queries that see the key unspecified, and
- * reaches no other.  A query that is not finite gets NaN (zeros if it sees no
- * key) and changes no other.
+ * counts with its sign; one that is not finite, or past 2^96 in magnitude, leaves
+ * the queries that see the key unspecified, and reaches no other.  A query that
+ * is not finite gets NaN (zeros if it sees no key) and changes no other.
  * A bounded wait that runs out inside the kernel for many queries is reported
  * by hadq_device_status; the workspace has to be zero-filled again after it.
  */

@@ -96,3 +96,14 @@ def test_large_value_scales(new, bits, e):
     c = Case(43, [(new, 300), (new, 90)], 4, 2, bits=bits)
     c.v[1][:] *= np.float32(2.0 ** e)
     held(c)
+
+
+# ------------------------------------------------------- signed key scales
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("bits,group", [(4, 128), (8, 32)])
+def test_negative_key_scales(new, bits, group):
+    """A key scale's sign counts in both kernels."""
+    c = Case(41, [(new, 300), (new, 90)], 4, 2, bits=bits, group=group)
+    c.k[1][:] *= np.where(c.rng.random(c.k[1].shape) < 0.5, -1.0, 1.0).astype(np.float32)
+    held(c)
