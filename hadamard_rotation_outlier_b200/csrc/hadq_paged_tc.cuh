@@ -457,11 +457,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           // the bound to [2^14, 2^15); a row whose entries are all below 2^-100
-          // counts as zero
+          // counts as zero, one that is not finite as NaN (an infinity alone
+          // could give every key the score -infinity, which reads as unseen)
           const float bound = __uint_as_float(mx << 16) * 128.f * a.qmul;
           const int be = min(int(__float_as_uint(bound) >> 23), 253);
           const int e = be < 27 ? 0 : 141 - be;
-          up[x] = be < 27 ? 0.f : a.qmul * pow2_clamped(e);
+          up[x] = mx >= 0x7F80u ? NAN : be < 27 ? 0.f : a.qmul * pow2_clamped(e);
           if (j == 0) tl->eq[m][r0 + 8 * x] = e;
         }
         float v[2][32];

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import paged_bounds as A
 from test_paged_bounds_gpu import held
 from test_paged_gpu import Case
 
@@ -107,3 +108,25 @@ def test_negative_key_scales(new, bits, group):
     c = Case(41, [(new, 300), (new, 90)], 4, 2, bits=bits, group=group)
     c.k[1][:] *= np.where(c.rng.random(c.k[1].shape) < 0.5, -1.0, 1.0).astype(np.float32)
     held(c)
+
+
+# ------------------------------------------- queries that are not finite
+
+@pytest.mark.parametrize("new", [5, 40])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_infinite_query_whose_scores_are_all_low(new, bits):
+    """An infinity in one column, against keys that give it the score minus
+    infinity: still NaN, and no other row changes."""
+    c = Case(42, [(new, new + 3), (new, 200)], 4, 2, bits=bits, with_signs=False)
+    c.k[0][c.table[0, :4]] = 0x99 if bits == 4 else 0x81   # code -7 or -127 in every column
+    c.k[1][:] = 0.01
+    want, rms = A.attention(c.q, c.k, c.v, c.table, c.lens, c.cu, c.page)
+    c.q[2, 1] = 0.0
+    c.q[2, 1, 0] = np.inf         # rotated: infinity in every column
+    c.q[3, 2] = 1.0
+    c.q[3, 2, 0] = np.inf
+    got = c.run()
+    for r, h in ((2, 1), (3, 2)):
+        assert np.isnan(got[r, h]).all()
+        want[r, h] = np.nan
+    A.check(got, want, rms)
