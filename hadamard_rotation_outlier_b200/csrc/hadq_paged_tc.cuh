@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
           // reference yet, the warp takes the maxima, raises references,
           // rescales O and does the weights again.
           uint32_t p[32];
-          float sum;
+          float sum = 0.f;
           for (bool fix = fresh;;) {
             float x[64];
 #pragma unroll
@@ -692,12 +692,15 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
               for (int k = 1; k < 63; k += 2) top = max3(top, x[k], x[k + 1]);
               top = fmaf(fmaxf(top, x[63]), f, vexp - kPagedRoom);
-              const bool need = top > M + kPtSlack;
+              // (a row that brought the warp here gets its own maximum, so that
+              // the tiles after do not: 64 weights of 2^8 stay below kPtWeights)
+              const bool need = top > M + kPtSlack || sum > kPtWeights;
               const float root = need ? exp2f(0.5f * (M - top)) : 1.f, alpha = root * root;
               if (need) M = top;
               l = l * root * root;
-              fresh = __any_sync(0xffffffffu, M == -INFINITY);
-              if (i > i0) {
+              // (but for rows that see nothing further on, and those of NaN)
+              fresh = __any_sync(0xffffffffu, M == -INFINITY && lim > t0 + kPtTile && top == top);
+              if (i > i0 && __any_sync(0xffffffffu, need)) {
                 wait(&tl->pv_done[m], (ns - 1) & 1);  // the tile before; S came after the one before that
                 tc_fence_after();
 #pragma unroll 1

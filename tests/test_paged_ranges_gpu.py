@@ -6,9 +6,11 @@ import numpy as np
 import pytest
 import torch
 
+import hadamard_rotation_outlier_b200 as hq
+
 import paged_bounds as A
 from test_paged_bounds_gpu import held
-from test_paged_gpu import Case
+from test_paged_gpu import Case, dev, dev_bf16
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -130,3 +132,51 @@ def test_infinite_query_whose_scores_are_all_low(new, bits):
         assert np.isnan(got[r, h]).all()
         want[r, h] = np.nan
     A.check(got, want, rms)
+
+
+# ------------------------------------------------ scores that rise with the position
+
+def rising(c, gain):
+    """Scores 0 in the first 64 keys of each request, `gain` log2 units after."""
+    c.signs = None
+    c.q[:] = 0.0
+    c.q[..., 0] = 8.0
+    c.k[0][:] = 0x77
+    c.k[1][:] = gain * np.log(2.0) / (7 * 8.0)
+    for b in range(len(c.lens)):
+        c.k[1][c.table[b, :64 // c.page]] = 0.0
+
+
+@pytest.mark.parametrize("gain", [0.0, 1.5, 3.0, 6.9, 9.0, -5.0])
+def test_rising_scores(gain):
+    c = Case(51, [(64, 700), (40, 900)], 2, 1)
+    rising(c, gain)
+    held(c)
+
+
+def test_rising_scores_cost_no_more():
+    """Scores that pass the first keys' by a few units leave the fast path once,
+    not in every tile after."""
+    c = Case(52, [(512, 4096)] * 4, 8, 2)
+    out = {}
+    for gain in (0.0, 3.0):
+        rising(c, gain)
+        args = [dev(x) for x in (c.k[0], c.k[1], c.v[0], c.v[1], c.table, c.lens, c.cu)]
+        q, ws = dev_bf16(c.q), torch.zeros(hq.hadq_paged_workspace_size(512, 8, 2), dtype=torch.uint8, device="cuda")
+        o = torch.empty_like(q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            hq.hadq_paged_attention(q, *args, 512, workspace=ws, out=o)
+        out[gain] = (g, args, q, ws, o)
+    best = {}
+    for _ in range(9):  # in turn, so that clocks and neighbours weigh on both
+        for gain, (g, *_) in out.items():
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                g.replay()
+            b.record()
+            b.synchronize()
+            best[gain] = min(best.get(gain, 1e9), a.elapsed_time(b))
+    assert best[3.0] <= 1.15 * best[0.0], best
