@@ -443,6 +443,12 @@ def _new(like, shape, dtype, stream, zero=False):
     return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
 
 
+def _int32(names, *values):
+    """Refuse numbers that a C int would wrap (2^32 + 32 would be a group of 32)."""
+    if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
+        raise ValueError(f"{names} must fit 32 bits, got {', '.join(map(str, values))}")
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -500,6 +506,7 @@ def hadq_paged_slots(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pag
     total_lens, cu_new, counts)`` with ``counts = [pages taken, requests
     refused]``; a refused request has total length 0 and slots -1.
     """
+    _int32("page_size", page_size)
     lib = load_library()
     index = _cuda(cached_lens, "cached_lens")
     batch = cached_lens.numel()
@@ -545,6 +552,7 @@ def hadq_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_c
     scales float32 ``[n_pages, n_kv_heads, page_size, 128/group]`` (the
     trailing 1 may be dropped).
     """
+    _int32("block, group and bits", block, group, bits)
     lib = load_library()
     index = _cuda(k, "k")
     dim = k.shape[-1] if k.dim() else 0
@@ -571,6 +579,7 @@ def hadq_paged_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Te
     Returns ``[tokens, n_kv_heads, 128]`` bf16 or fp32.  Rows whose slot is
     outside the pool are left as they were (of a new ``out``: undefined).
     """
+    _int32("block, group and bits", block, group, bits)
     lib = load_library()
     index = _cuda(codes, "codes")
     shape = _pool(codes, scales, "pool", index, bits, _resolve(128, block, group))
@@ -594,6 +603,7 @@ def hadq_paged_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Te
 
 def hadq_paged_workspace_size(max_new: int, n_q_heads: int, n_kv_heads: int) -> int:
     """Host-only: workspace bytes :func:`hadq_paged_attention` needs (any GPU, batch and lengths)."""
+    _int32("max_new, n_q_heads and n_kv_heads", max_new, n_q_heads, n_kv_heads)
     n = ctypes.c_size_t(0)
     _check(load_library().hadq_paged_workspace_size(max_new, n_q_heads, n_kv_heads, ctypes.byref(n)))
     return int(n.value)
@@ -619,6 +629,7 @@ def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch
     n_q_heads, 128]``; rows behind the last request are left as they were (of a
     new ``out``: undefined).  ``out`` may be ``q`` itself.
     """
+    _int32("max_new, block, group, bits, window and sinks", max_new, block, group, bits, window, sinks)
     lib = load_library()
     index = _cuda(q, "q")
     stride = _rows_view(q, "q", index, None)
@@ -634,8 +645,6 @@ def hadq_paged_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch
     _on(block_table, "block_table", _I32, index)
     if signs is not None:
         _on(signs, "signs", _I8, index, (dim,))
-    if max(window, sinks, max_new) > 0x7FFFFFFF:  # (a C int would wrap)
-        raise ValueError("window, sinks and max_new must be below 2^31")
     if softmax_scale is None:
         softmax_scale = 1.0 / float(dim) ** 0.5
     if out is None:
