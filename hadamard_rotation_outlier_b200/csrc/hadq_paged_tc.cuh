@@ -865,9 +865,13 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
           for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), y ? kPagedExpHigh : 227);
           int low = kPagedExpLow;
-          if (i > it.i0) {  // the tile before, of the other warp (which publishes no further one before this)
+          if (n > 0) {
+            // The tile before, of the other warp: for its limit, and (at a
+            // unit's first tile too) so that neither warp gets two of its tiles
+            // ahead of the other's next, where this barrier's phase would have
+            // passed before it is looked at.
             wait(&tl->plan_full[(n - 1) % kPtPlans], ((n - 1) / kPtPlans) & 1);
-            low = int(tl->info[(n - 1) % kPtInfos] >> 24);
+            if (i > it.i0) low = int(tl->info[(n - 1) % kPtInfos] >> 24);
           }
           e[1] = max(e[1], low);
           low = max(low, e[1] - kPagedExpSpan);

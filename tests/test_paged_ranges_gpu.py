@@ -180,3 +180,16 @@ def test_rising_scores_cost_no_more():
             b.synchronize()
             best[gain] = min(best.get(gain, 1e9), a.elapsed_time(b))
     assert best[3.0] <= 1.15 * best[0.0], best
+
+
+# ----------------------------------------------------------- short units
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_many_units_of_one_to_three_tiles(bits):
+    """The warps that plan tiles ahead pass from unit to unit without waiting
+    for the rows: no wait may be left behind."""
+    rng = np.random.default_rng(bits)
+    lens = rng.integers(40, 190, 700)
+    c = Case(53, [(34 + b % 7, int(n)) for b, n in enumerate(lens)], 1, 1, bits=bits)
+    held(c)
+    hq.hadq_device_status()  # (raises if a wait ran out)
