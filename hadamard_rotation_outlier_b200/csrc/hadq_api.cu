@@ -1396,9 +1396,15 @@ constexpr size_t kPagedCounterBytes = 8192;
 static size_t paged_part_bytes(int64_t ctas, int rows) { return size_t(ctas) * 2 * rows * (hadq::kPagedDim + 2) * sizeof(float); }
 
 // Requests of up to this many query rows per KV head go to the kernel for few
-// rows, whose time goes by rows / 16: with 32 requests of 4000 INT4 keys and 8
-// KV heads, 16 / 32 rows take 66 / 115 us there against 144 us for any count up
-// to 128 in the kernel for many (INT8, 32 rows: 126 against 151 us).
+// rows, whose time goes by rows / 16, where that of the kernel for many is the
+// same for any count up to 128.  us, few / many, 8 KV heads:
+//   rows                            16          32          48
+//   32 requests x 4000 keys INT4  68 / 144   117 / 148   164 / 149
+//                           INT8  74 / 152   127 / 154   177 / 155
+//   256 x 300               INT4  89 / 149   171 / 167   252 / 163
+//   1 x 131072              INT4  75 / 159   109 / 160   148 / 161
+//                           INT8  81 / 167   120 / 167   163 / 168
+// So the border lies between 32 and 48 rows for long and for short requests.
 constexpr int kPagedFewRows = 32;
 static bool paged_uses_chunk(int64_t max_rows, int g) { return max_rows > kPagedFewRows && g <= hadq::kPtRows; }
 

@@ -229,7 +229,7 @@ __device__ __forceinline__ void h16_operand(int g, int j, int c, uint32_t one, u
 // codes per group, stored at the token's slot.  Reads 256 bytes and writes
 // 16 * BITS + 512 / G per row: bound by HBM (a row is 2.6 bytes per element
 // for INT4, 3.1 for INT8, against about 6 instructions per 32 elements).
-// 131072 tokens x 8 heads INT4: 133 us (0.81 of the copy rate); 4099 x 32 INT8, groups of
+// 131072 tokens x 8 heads INT4: 133 us (0.79 of the copy rate); 4099 x 32 INT8, groups of
 // 64: 17.7 us.
 // Lane (g, j) holds elements 32 j .. 32 j + 31 of rows g and g + 8: its codes
 // leave as one (INT4) or two 16-byte stores with nothing exchanged, and a

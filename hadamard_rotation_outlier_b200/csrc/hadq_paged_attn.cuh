@@ -182,11 +182,12 @@ __device__ __forceinline__ PagedPiece paged_plan(const PagedAttnArgs& a, PagedPl
 // in: m = max(score + e) - 8 when it was last raised, so an f16 weight is below
 // 2^16 whatever the scales are; l and O are float32.
 //
-// Bound by HBM for long INT8 caches and by the issue rate for INT4: a cached
-// row pair is 2 * (16 BITS + 512 / G) bytes against about 13 warp
-// instructions, most of them for the value codes.  64 ragged requests of 17 to
-// 8191 keys, 32 query and 8 KV heads: INT8 118 us (0.84 of the copy rate), INT4
-// 94 us (0.54); one request over 131072 INT4 keys 46 us.
+// Bound by HBM for long INT8 caches.  INT4 uses up no rate (issue 55 %, ALU 46 %,
+// DRAM 36 %): about 690 warp instructions per 32 keys, most of them for the
+// value codes, form one chain (scores, maximum, exponents, value product), and
+// the three CTAs that an SM's registers hold wait on it.  64 ragged requests of
+// 17 to 8191 keys, 32 query and 8 KV heads: INT8 117 us (0.84 of the copy rate),
+// INT4 94 us (0.54); one request over 131072 INT4 keys 46-48 us.
 constexpr int kPdThreads = 128;
 constexpr int kPdWarps = 4;
 constexpr int kPdStep = 32;                     // keys per warp and step

@@ -46,14 +46,15 @@
 // Bound: 4 * 64 * 256 * 128 flops per tile take 1024 cycles at the dense f16
 // rate, the 2 * 128 * 64 exponentials as long at 16 a cycle, and the operands'
 // 128 KB of shared-memory traffic as long at 128 bytes a cycle.  Measured are
-// 2100 cycles a tile: 760 us for 4 requests of 1500-2048 queries x 32 heads
-// over 2000-8192 INT4 keys x 8 heads, 0.54 of cuBLAS's bf16 rate.  What fills
+// 2100 cycles a tile: 760-780 us for 4 requests of 1500-2048 queries x 32 heads
+// over 2000-8192 INT4 keys x 8 heads, 0.53 of cuBLAS's bf16 rate.  What fills
 // the rest is the chain of one row's softmax (read S, 64 exponentials, sum,
 // convert, write P) against which two groups hide too little, and the switch
 // between units (17,000 cycles: 7000 for queries, 6000 for a join, 5000 to
 // finish).  The next unit's queries are therefore brought to L2 a unit ahead
 // and loaded 64 bytes of a row at a time, and rows leave in 32-byte stores (16
-// requests of 512 tokens: 156 -> 140 us, cross attention 165 -> 154 us).
+// requests of 512 tokens: 156 -> 140 us, cross attention 165 -> 154 us; now 132
+// and 159-164 us).
 //
 // Every mbarrier wait gives up after about a second: the kernel then records a
 // fault (hadq_device_status reads it); every role runs on to its end without

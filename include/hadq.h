@@ -490,8 +490,10 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  * hadq_paged_attention -- attention of each request's new tokens over its
  * pages: single tokens (decoding), several (speculative tokens, prompt chunks)
  * and, with causal 0, queries over the cached states of another sequence
- * (cross attention).  The arithmetic is that of hadq_kv_decode_attention; the
- * new tokens' own K and V are in the cache before the call.
+ * (cross attention).  The formula is that of hadq_kv_decode_attention, at fewer
+ * bits (below): that call, for one token over a contiguous cache, rounds to
+ * nothing less than float32.  The new tokens' own K and V are in the cache
+ * before the call.
  *
  *   q            device bf16 [q_rows, n_q_heads, dim] with q_stride elements
  *                from one row to the next, at least n_q_heads * dim and a
@@ -504,8 +506,9 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *   total_lens   device int32 [batch]: cached tokens, the new ones among them
  *                when causal.
  *   max_new      upper bound of the requests' query counts, known to the host:
- *                it chooses the kernels and the workspace size, not the
- *                result.
+ *                it chooses the kernels (one for requests of up to 32 query
+ *                rows per KV head, one for more) and the workspace size: of
+ *                the result it changes the roundings only.
  *   block_table  device int32 [batch, max_pages], max_pages * page_size at
  *                most 2^30 (longer requests are cut to that room), the pool's
  *                rows n_pages * page_size * n_kv_heads below 2^32.  Keys on a
@@ -526,10 +529,15 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  *                call leaves it ready for the next.  Calls that share one must
  *                be ordered (also two captured graphs that do).
  *
- * Softmax statistics and sums are float32; the rotated query enters the score
- * product with at least 11 significant bits.  A weight enters the value product
- * with 11 significant bits down to 2^-22 of its row's largest, and with an error
- * of 2^-33 of the largest below that.
+ * Roundings: softmax statistics and sums are float32, the result bf16.  Up to 32
+ * query rows per KV head the rotated query is 16-bit fixed point, and a weight
+ * times its value scale has 11 significant bits; codes and key scales count in
+ * full.  With more, the rotated query, the weights, the scales and the scaled
+ * codes of keys and values have 11 bits each, the scales relative to the largest
+ * in their tile: a key's score is then off by up to 2^-11 of itself (0.02 at a
+ * score of 50), where a result that hangs on two keys follows it.  Weights keep
+ * their 11 bits down to 2^-22 of their row's largest, and below that have an
+ * error of 2^-33 of the largest.
  * A value scale that is negative or not finite counts as zero, and so do, next
  * to the other keys, value scales below 2^-22 of the largest in their tile (32
  * or 64 keys) or below 2^-60 of the largest in their request, and scales and
