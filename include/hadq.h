@@ -540,11 +540,13 @@ hadq_status hadq_paged_gather(const void *codes, const float *scales, int64_t n_
  * error of 2^-33 of the largest.
  * A value scale that is negative or not finite counts as zero, and so do, next
  * to the other keys, value scales below 2^-22 of the largest in their tile (32
- * or 64 keys) or below 2^-60 of the largest in their request, and scales and
- * queries below 2^-100; such a key keeps its weight in the sum.  A key scale
- * counts with its sign; one that is not finite, or past 2^96 in magnitude, leaves
- * the queries that see the key unspecified, and reaches no other.  A query that
- * is not finite gets NaN (zeros if it sees no key) and changes no other.
+ * or 64 keys, seen by the query or not) or below 2^-60 of the largest in their
+ * request, and scales and queries below 2^-100; such a key keeps its weight in
+ * the sum.  With more than 32 rows, key scales below 2^-22 of the largest in
+ * their tile count as zero as well.  A key scale counts with its sign; one that
+ * is not finite, or past 2^96 in magnitude, leaves the queries that see the key
+ * unspecified, and reaches no other.  A query that is not finite gets NaN (zeros
+ * if it sees no key) and changes no other.
  * A bounded wait that runs out inside the kernel for many queries is reported
  * by hadq_device_status; the workspace has to be zero-filled again after it.
  */
