@@ -857,14 +857,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_chunk_kernel(const PagedA
 #pragma unroll
             for (int q = 0; q < NG; ++q) {
               const float k = row[x] != ~0u ? __ldg(a.k_scales + int64_t(row[x]) * NG + q) : 0.f;
-              sc[0][x][q] = fabsf(k) < INFINITY ? k : 0.f;  // (signed; what one that is not finite gives is open)
+              // signed; what one past 2^96 or not finite gives is open, but it
+              // must not set the tile's exponent, which all queries share
+              sc[0][x][q] = fabsf(k) <= 7.9228163e28f ? k : 0.f;
               sc[1][x][q] = row[x] != ~0u ? clean_scale(__ldg(a.v_scales + int64_t(row[x]) * NG + q)) : 0.f;
               top[0] = fmaxf(top[0], fabsf(sc[0][x][q]));
               top[1] = fmaxf(top[1], sc[1][x][q]);
             }
           int e[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), y ? kPagedExpHigh : 227);
+          for (int y = 0; y < 2; ++y) e[y] = min(max(int(__reduce_max_sync(0xffffffffu, __float_as_uint(top[y])) >> 23), 27), kPagedExpHigh);
           int low = kPagedExpLow;
           if (n > 0) {
             // The tile before, of the other warp: for its limit, and (at a

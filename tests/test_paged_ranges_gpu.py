@@ -193,3 +193,15 @@ def test_many_units_of_one_to_three_tiles(bits):
     c = Case(53, [(34 + b % 7, int(n)) for b, n in enumerate(lens)], 1, 1, bits=bits)
     held(c)
     hq.hadq_device_status()  # (raises if a wait ran out)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [1e30, np.inf, np.nan])
+def test_key_scale_past_the_limit_reaches_no_other_query(new, scale):
+    """The last token's key scale, which only its own query sees."""
+    c = Case(54, [(new, 300), (new, 90)], 4, 2, bits=8)
+    want, rms = A.attention(c.q, c.k, c.v, c.table, c.lens, c.cu, c.page, signs=c.signs)
+    for b, n in enumerate(c.lens):
+        c.k[1][c.table[b, (n - 1) // c.page], :, (n - 1) % c.page] = scale
+        want[c.cu[b + 1] - 1] = np.nan
+    A.check(c.run(), want, rms)
